@@ -9,6 +9,10 @@
  *   copy_page_indices             block-table rows -> flat page list, through an indptr
  *   compute_num_kv_splits         per-sequence split count
  *
+ * Around it: paged_kv_write and paged_kv_read move tokens into and out of the
+ * caches, paged_attention_tree attends from drafted token trees; the metadata
+ * steps and the split-KV decode without caller scratch follow further down.
+ *
  * Conventions shared by every entry point
  * ----------------------------------------
  * - Every pointer argument is DEVICE memory owned and allocated by the caller.
@@ -156,7 +160,7 @@ typedef struct {
   const int32_t *seq_order;
 } pkv_decode_args_t;
 
-/* Library version string, e.g. "paged_kv 0.2.0 sm_103a". */
+/* Library version string, e.g. "paged_kv 0.3.0 sm_103a". */
 const char *pkv_version(void);
 /* Static description of a status code. */
 const char *pkv_status_string(pkv_status_t status);
@@ -519,6 +523,173 @@ size_t pkv_noalloc_scratch_bytes(void);
  */
 pkv_status_t pkv_order_by_length(int32_t *order, const int32_t *seq_lens, int32_t num_seqs,
                                  pkv_stream_t stream);
+
+/*
+ * Writing tokens into the caches, quantising them where the caches are 8-bit.
+ *
+ * For every token i < num_tokens with slot = slot_mapping[i] >= 0, block =
+ * slot / block_size, off = slot % block_size, every kv head h and head dim d:
+ *   key_cache[block, h, d / x, off, d % x] = store(key[i, h, d], k_scale)
+ *   value_cache[block, h, d, off]          = store(value[i, h, d], v_scale)
+ * store(y, scale) = y itself for PKV_KV_AUTO; for an 8-bit cache the code of
+ * the format nearest to y / scale (an fp32 division; ties to the even code;
+ * magnitudes beyond the largest finite value, infinities too, become that
+ * value; NaN becomes a NaN code): the inverse of what the attention entry
+ * points read, decode(code) * scale.
+ *
+ * A negative slot is padding: nothing is written for its token.  A slot at or
+ * past num_blocks * block_size is skipped and sets PKV_ERRF_BLOCK_ID.  The
+ * other slots of the caches are left as they were.  Two tokens with the same
+ * slot leave it with elements of either.  The caches may not overlap the inputs.
+ *
+ *   key, value: [num_tokens, num_kv_heads, head_size] in dtype; the elements of
+ *       a head adjacent (stride[2] == 1), the other strides free (views of a
+ *       joint projection).  Token rows on 16-byte boundaries are read 16 bytes
+ *       at a time, others element by element.
+ *   slot_mapping: [num_tokens] int64, slot_stride apart.
+ * Caches, strides, types and sizes as for paged_attention_decode (head_size 64,
+ * 128, 256, with fp32 64 and 128; block_size 8, 16, 32; 8-bit caches from fp16
+ * / bf16); scales of 8-bit caches finite and positive.  num_kv_heads <= 65535.
+ */
+typedef struct {
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t head_size;
+  int32_t block_size;
+  int32_t x;
+  int32_t num_blocks;
+  pkv_dtype_t dtype;
+  int32_t kv_cache_dtype; /* pkv_kv_cache_dtype_t */
+  float k_scale;
+  float v_scale;
+  const void *key;
+  int64_t key_stride[3];
+  const void *value;
+  int64_t value_stride[3];
+  void *key_cache;
+  int64_t k_stride[5];
+  void *value_cache;
+  int64_t v_stride[4];
+  const int64_t *slot_mapping;
+  int64_t slot_stride;
+  int32_t *err_flag; /* optional */
+} pkv_cache_write_args_t;
+
+pkv_status_t paged_kv_write(const pkv_cache_write_args_t *args, pkv_stream_t stream);
+/* sizeof(pkv_cache_write_args_t), for bindings that mirror the struct. */
+size_t pkv_cache_write_args_size(void);
+
+/*
+ * Reading sequences back out of the caches, dequantised, packed one behind
+ * the other.  For every sequence s and 0 <= i < cu_seq_lens[s+1] -
+ * cu_seq_lens[s], with t = seq_starts[s] + i (seq_starts NULL: t = i):
+ *   key_out[cu_seq_lens[s] + i, h, :]   = K of token t of s, kv head h
+ *   value_out[cu_seq_lens[s] + i, h, :] = V of token t of s, kv head h
+ * An 8-bit element stands for decode(code) * scale, computed in fp32 and
+ * rounded once to dtype; other caches are copied.  Rows that no sequence
+ * covers are left untouched.
+ *
+ *   key_out, value_out: [num_tokens, num_kv_heads, head_size] in dtype, the
+ *       elements of a head adjacent, the other strides free.
+ *   block_tables, bt_stride, kv_indptr, max_blocks_per_seq, num_blocks: as for
+ *       paged_attention_decode.
+ *   cu_seq_lens: [num_seqs + 1] int32, not descending, starting at 0; a row that
+ *       descends or leaves [0, num_tokens] is skipped and sets PKV_ERRF_INDPTR.
+ *   seq_starts: optional [num_seqs] int32.  Tokens before 0 or past the row's
+ *       pages are not written and set PKV_ERRF_SEQ_LEN.
+ * Types and sizes as for paged_kv_write.  num_seqs <= 65535.
+ */
+typedef struct {
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t head_size;
+  int32_t block_size;
+  int32_t x;
+  int32_t num_blocks;
+  int32_t max_blocks_per_seq;
+  pkv_dtype_t dtype;
+  int32_t kv_cache_dtype; /* pkv_kv_cache_dtype_t */
+  float k_scale;
+  float v_scale;
+  void *key_out;
+  int64_t key_stride[3];
+  void *value_out;
+  int64_t value_stride[3];
+  const void *key_cache;
+  int64_t k_stride[5];
+  const void *value_cache;
+  int64_t v_stride[4];
+  const int32_t *block_tables;
+  int64_t bt_stride[2];
+  const int32_t *kv_indptr;   /* optional */
+  const int32_t *cu_seq_lens;
+  const int32_t *seq_starts;  /* optional */
+  int32_t *err_flag;          /* optional */
+} pkv_cache_read_args_t;
+
+pkv_status_t paged_kv_read(const pkv_cache_read_args_t *args, pkv_stream_t stream);
+/* sizeof(pkv_cache_read_args_t), for bindings that mirror the struct. */
+size_t pkv_cache_read_args_size(void);
+
+/*
+ * Attention of drafted token trees over the paged cache (the verification step
+ * of speculative decoding; with one drafted token a sequence, a decode step).
+ *
+ * Sequence s brings T_s = cu_query_lens[s+1] - cu_query_lens[s] drafted tokens,
+ * any number from 0 on.  Their keys and values are in the cache already, as
+ * the last T_s of its seq_lens[s] tokens (paged_kv_write), in the order of
+ * their query rows.  With ctx = seq_lens[s] - T_s, the query row of drafted
+ * token i sees every token t < ctx and those drafted tokens j (t = ctx + j) with
+ *   tree_mask[row, j] != 0, or, without a tree_mask, j <= i (a chain).
+ * A tree is given by each row's ancestors and itself; any other mask works too.
+ * For every row and query head h, over the tokens t that the row sees:
+ *   z_t = scale * (q . k_t)
+ *   z_t = cap * tanh(z_t / cap)                       if cap = logits_soft_cap > 0
+ *   z_t = z_t + alibi_slopes[h] * (pos(t) - pos(row))  if alibi_slopes
+ *   out[row, h, :] = sum_t softmax_t(z) v_t
+ * pos(t) = t before ctx; a drafted token's is positions[its row], or ctx + its
+ * place without positions (only read with alibi_slopes).  A row that sees
+ * nothing gets zeros.  What a row does not see has no part in its result,
+ * whatever stands there (NaN and infinities too).
+ *
+ *   args: as for paged_attention_decode, but that query is [num_tokens,
+ *       num_heads, head_size], the drafted tokens of all sequences one behind
+ *       the other; num_seqs counts sequences.  seq_order is not used.
+ *   out: [num_tokens, num_heads, head_size] in args->dtype, strides out_stride;
+ *       rows past cu_query_lens[num_seqs] are left untouched.
+ *   cu_query_lens: [num_seqs + 1] int32, not descending.  A row that is negative,
+ *       descends or passes num_tokens makes its sequence empty and sets
+ *       PKV_ERRF_INDPTR.  seq_lens[s] < T_s sets PKV_ERRF_SEQ_LEN.
+ *   tree_mask: optional [num_tokens, mask_cols] bytes, any strides (a zero row
+ *       stride shares one row); columns past mask_cols count as 0.
+ *   positions: optional [num_tokens] int32.
+ *   workspace: pkv_tree_workspace_bytes(head_size) bytes of device memory on a
+ *       256-byte boundary, for the partial results of sequences that several
+ *       CTAs share.  Its size depends on the GPU and the head size only.  Nothing
+ *       in it outlives the call; calls that overlap on the GPU need one each.
+ * K and V are read once per 128 query rows of a kv head (fp32: 32).
+ * Types, sizes and errors as for paged_attention_decode.
+ */
+typedef struct {
+  int32_t num_tokens;
+  int32_t mask_cols;
+  const int32_t *cu_query_lens;
+  const uint8_t *tree_mask; /* optional */
+  int64_t mask_stride[2];
+  const int32_t *positions; /* optional */
+  float logits_soft_cap;    /* 0: none */
+  void *workspace;
+  size_t workspace_bytes;
+} pkv_tree_args_t;
+
+pkv_status_t paged_attention_tree(void *out, const int64_t out_stride[3],
+                                  const pkv_decode_args_t *args, const pkv_tree_args_t *tree,
+                                  pkv_stream_t stream);
+/* Bytes of paged_attention_tree's workspace on the current device. */
+size_t pkv_tree_workspace_bytes(int32_t head_size);
+/* sizeof(pkv_tree_args_t), for bindings that mirror the struct. */
+size_t pkv_tree_args_size(void);
 
 #ifdef __cplusplus
 } /* extern "C" */

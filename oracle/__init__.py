@@ -18,6 +18,7 @@ from .attention import (  # noqa: F401
     v2_partition,
     v2_reduce,
 )
+from .cache import encode, kv_read, kv_write  # noqa: F401
 from .metadata import (  # noqa: F401
     cdiv,
     copy_page_indices,
@@ -29,3 +30,4 @@ from .metadata import (  # noqa: F401
     swa_spec_page_table,
     wrap_int32,
 )
+from .tree import tree_attention  # noqa: F401

@@ -38,6 +38,10 @@ __all__ = [
     "paged_attention_v2_noalloc",
     "noalloc_scratch_bytes",
     "order_by_length",
+    "paged_kv_write",
+    "paged_kv_read",
+    "paged_attention_tree",
+    "tree_workspace_bytes",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -113,6 +117,47 @@ class SwaSpecArgs(ctypes.Structure):
     ]
 
 
+class CacheWriteArgs(ctypes.Structure):
+    """Mirror of ``pkv_cache_write_args_t``."""
+
+    _fields_ = [
+        ("num_tokens", _c_i32), ("num_kv_heads", _c_i32), ("head_size", _c_i32),
+        ("block_size", _c_i32), ("x", _c_i32), ("num_blocks", _c_i32), ("dtype", ctypes.c_int),
+        ("kv_cache_dtype", _c_i32), ("k_scale", _c_f32), ("v_scale", _c_f32),
+        ("key", _c_p), ("key_stride", _c_i64 * 3), ("value", _c_p), ("value_stride", _c_i64 * 3),
+        ("key_cache", _c_p), ("k_stride", _c_i64 * 5),
+        ("value_cache", _c_p), ("v_stride", _c_i64 * 4),
+        ("slot_mapping", _c_p), ("slot_stride", _c_i64), ("err_flag", _c_p),
+    ]
+
+
+class CacheReadArgs(ctypes.Structure):
+    """Mirror of ``pkv_cache_read_args_t``."""
+
+    _fields_ = [
+        ("num_seqs", _c_i32), ("num_tokens", _c_i32), ("num_kv_heads", _c_i32),
+        ("head_size", _c_i32), ("block_size", _c_i32), ("x", _c_i32), ("num_blocks", _c_i32),
+        ("max_blocks_per_seq", _c_i32), ("dtype", ctypes.c_int), ("kv_cache_dtype", _c_i32),
+        ("k_scale", _c_f32), ("v_scale", _c_f32),
+        ("key_out", _c_p), ("key_stride", _c_i64 * 3),
+        ("value_out", _c_p), ("value_stride", _c_i64 * 3),
+        ("key_cache", _c_p), ("k_stride", _c_i64 * 5),
+        ("value_cache", _c_p), ("v_stride", _c_i64 * 4),
+        ("block_tables", _c_p), ("bt_stride", _c_i64 * 2),
+        ("kv_indptr", _c_p), ("cu_seq_lens", _c_p), ("seq_starts", _c_p), ("err_flag", _c_p),
+    ]
+
+
+class TreeArgs(ctypes.Structure):
+    """Mirror of ``pkv_tree_args_t``."""
+
+    _fields_ = [
+        ("num_tokens", _c_i32), ("mask_cols", _c_i32), ("cu_query_lens", _c_p),
+        ("tree_mask", _c_p), ("mask_stride", _c_i64 * 2), ("positions", _c_p),
+        ("logits_soft_cap", _c_f32), ("workspace", _c_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _LIB = None
 
 
@@ -185,6 +230,21 @@ def lib() -> ctypes.CDLL:
                                              ctypes.POINTER(DecodeArgs), _c_p]
     L.pkv_noalloc_scratch_bytes.restype = ctypes.c_size_t
     L.pkv_noalloc_scratch_bytes.argtypes = []
+    for name, struct in (("cache_write", CacheWriteArgs), ("cache_read", CacheReadArgs),
+                         ("tree", TreeArgs)):
+        size = getattr(L, f"pkv_{name}_args_size")
+        size.restype, size.argtypes = ctypes.c_size_t, []
+        if size() != ctypes.sizeof(struct):
+            raise RuntimeError(f"pkv_{name}_args_t layout mismatch")
+    L.paged_kv_write.restype = ctypes.c_int
+    L.paged_kv_write.argtypes = [ctypes.POINTER(CacheWriteArgs), _c_p]
+    L.paged_kv_read.restype = ctypes.c_int
+    L.paged_kv_read.argtypes = [ctypes.POINTER(CacheReadArgs), _c_p]
+    L.paged_attention_tree.restype = ctypes.c_int
+    L.paged_attention_tree.argtypes = [_c_p, ctypes.POINTER(_c_i64), ctypes.POINTER(DecodeArgs),
+                                       ctypes.POINTER(TreeArgs), _c_p]
+    L.pkv_tree_workspace_bytes.restype = ctypes.c_size_t
+    L.pkv_tree_workspace_bytes.argtypes = [_c_i32]
     if L.pkv_decode_args_size() != ctypes.sizeof(DecodeArgs):
         raise RuntimeError("pkv_decode_args_t layout mismatch between the library and the binding")
     _LIB = L
@@ -643,3 +703,206 @@ def paged_attention_v2_noalloc(out: torch.Tensor, query: torch.Tensor, key_cache
                                             int(partition_size), _ptr(num_kv_splits),
                                             ctypes.byref(a), _stream(stream)),
            "paged_attention_v2_noalloc")
+
+
+def _same_device(first: torch.Tensor, *named) -> torch.device:
+    """The one CUDA device of all tensors (None entries are skipped)."""
+    dev = first.device
+    for t, n in named:
+        _cuda(t, n)
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, not on {dev}")
+    return dev
+
+
+def _call_on(dev: torch.device, stream, what: str, call) -> None:
+    """``call(stream)`` with ``dev`` current, on ``stream`` or that device's current stream."""
+    if dev.index == torch.cuda.current_device():
+        _check(call(_stream(stream)), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(call(_stream(stream)), what)
+
+
+def _fill_strides(array, t: torch.Tensor) -> None:
+    for i, s in enumerate(t.stride()):
+        array[i] = s
+
+
+def _cache_io_args(a, key, value, names, key_cache, value_cache, kv_cache_dtype, k_scale,
+                   v_scale) -> None:
+    """Fields that ``CacheWriteArgs`` and ``CacheReadArgs`` share."""
+    if key.dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {key.dtype}")
+    if value.dtype != key.dtype:
+        raise ValueError(f"{names[0]} and {names[1]} must share a dtype")
+    if key.dim() != 3 or key_cache.dim() != 5 or value_cache.dim() != 4:
+        raise ValueError(f"expected {names[0]} and {names[1]} [N,Hk,D], key_cache [NB,Hk,D/x,bs,x], "
+                         "value_cache [NB,Hk,D,bs]")
+    nb, hk, dx, bs, x = key_cache.shape
+    if tuple(value_cache.shape) != (nb, hk, dx * x, bs):
+        raise ValueError("key_cache and value_cache do not belong together")
+    if key.shape != value.shape or tuple(key.shape[1:]) != (hk, dx * x):
+        raise ValueError(f"{names[0]} and {names[1]} must be [N, {hk}, {dx * x}] for these caches")
+    a.num_tokens, a.num_kv_heads, a.head_size = key.shape
+    a.block_size, a.x, a.num_blocks = bs, x, nb
+    a.dtype = _DTYPE_CODE[key.dtype]
+    a.kv_cache_dtype = _kv_cache_code(key_cache, value_cache, key, kv_cache_dtype)
+    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
+    _fill_strides(a.key_stride, key)
+    _fill_strides(a.value_stride, value)
+    a.key_cache, a.value_cache = _ptr(key_cache), _ptr(value_cache)
+    _fill_strides(a.k_stride, key_cache)
+    _fill_strides(a.v_stride, value_cache)
+
+
+def paged_kv_write(key_cache: torch.Tensor, value_cache: torch.Tensor, key: torch.Tensor,
+                   value: torch.Tensor, slot_mapping: torch.Tensor, *, kv_cache_dtype: str = "auto",
+                   k_scale: float = 1.0, v_scale: float = 1.0,
+                   err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write tokens into the caches: ``key`` / ``value [N, num_kv_heads, head_size]``
+    to slots ``slot_mapping`` (int64 ``[N]``: block * block_size + slot in the
+    block; negative: not written).  8-bit caches get the nearest code of
+    ``x / scale``, saturating; see ``paged_kv_write`` in the header."""
+    _cuda(key_cache, "key_cache")
+    dev = _same_device(key_cache, (value_cache, "value_cache"), (key, "key"), (value, "value"),
+                       (slot_mapping, "slot_mapping"), (err_flag, "err_flag"))
+    a = CacheWriteArgs()
+    _cache_io_args(a, key, value, ("key", "value"), key_cache, value_cache, kv_cache_dtype,
+                   k_scale, v_scale)
+    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (key.shape[0],):
+        raise ValueError("slot_mapping must be int64 [N]")
+    if err_flag is not None and err_flag.dtype != torch.int32:
+        raise ValueError("err_flag must be int32")
+    a.key, a.value = _ptr(key), _ptr(value)
+    a.slot_mapping, a.slot_stride = _ptr(slot_mapping), slot_mapping.stride(0)
+    a.err_flag = _ptr(err_flag)
+    _call_on(dev, stream, "paged_kv_write", lambda s: lib().paged_kv_write(ctypes.byref(a), s))
+
+
+def paged_kv_read(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: torch.Tensor,
+                  value_cache: torch.Tensor, block_tables: torch.Tensor, cu_seq_lens: torch.Tensor,
+                  *, seq_starts: Optional[torch.Tensor] = None,
+                  kv_indptr: Optional[torch.Tensor] = None,
+                  err_flag: Optional[torch.Tensor] = None,
+                  max_blocks_per_seq: Optional[int] = None, kv_cache_dtype: str = "auto",
+                  k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """Read tokens ``seq_starts[s] .. + cu_seq_lens[s+1] - cu_seq_lens[s]`` of every
+    sequence back into ``key_out`` / ``value_out [N, num_kv_heads, head_size]``,
+    packed at ``cu_seq_lens`` (int32 ``[B + 1]``), 8-bit codes as ``code * scale``."""
+    _cuda(key_cache, "key_cache")
+    dev = _same_device(key_cache, (value_cache, "value_cache"), (key_out, "key_out"),
+                       (value_out, "value_out"), (block_tables, "block_tables"),
+                       (cu_seq_lens, "cu_seq_lens"), (seq_starts, "seq_starts"),
+                       (kv_indptr, "kv_indptr"), (err_flag, "err_flag"))
+    a = CacheReadArgs()
+    _cache_io_args(a, key_out, value_out, ("key_out", "value_out"), key_cache, value_cache,
+                   kv_cache_dtype, k_scale, v_scale)
+    for t, n in ((block_tables, "block_tables"), (cu_seq_lens, "cu_seq_lens"),
+                 (seq_starts, "seq_starts"), (kv_indptr, "kv_indptr"), (err_flag, "err_flag")):
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{n} must be int32")
+    a.num_seqs = cu_seq_lens.numel() - 1
+    _check_rows(cu_seq_lens, "cu_seq_lens", a.num_seqs + 1)
+    _check_rows(seq_starts, "seq_starts", a.num_seqs)
+    _fill_tables(a, block_tables, kv_indptr, max_blocks_per_seq)
+    a.key_out, a.value_out = _ptr(key_out), _ptr(value_out)
+    a.cu_seq_lens, a.seq_starts = _ptr(cu_seq_lens), _ptr(seq_starts)
+    a.err_flag = _ptr(err_flag)
+    _call_on(dev, stream, "paged_kv_read", lambda s: lib().paged_kv_read(ctypes.byref(a), s))
+
+
+def _check_rows(t: Optional[torch.Tensor], name: str, n: int) -> None:
+    if t is not None and (n < 0 or tuple(t.shape) != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous [{max(n, 1)}] tensor")
+
+
+def _fill_tables(a, block_tables, kv_indptr, max_blocks_per_seq) -> None:
+    """Block-table fields: a 2-D table, or the flat page list of ``kv_indptr``."""
+    if kv_indptr is None:
+        if block_tables.dim() != 2 or block_tables.shape[0] < a.num_seqs:
+            raise ValueError("block_tables must be 2-D [num_seqs, max_blocks_per_seq]")
+        cols = block_tables.shape[1]
+        a.max_blocks_per_seq = cols if max_blocks_per_seq is None else int(max_blocks_per_seq)
+        if a.max_blocks_per_seq > cols:
+            raise ValueError("max_blocks_per_seq exceeds block_tables' columns")
+        _fill_strides(a.bt_stride, block_tables)
+    else:
+        if block_tables.dim() != 1:
+            raise ValueError("with kv_indptr, block_tables is the flat page list (1-D)")
+        _check_rows(kv_indptr, "kv_indptr", a.num_seqs + 1)
+        a.bt_stride[0], a.bt_stride[1] = 0, block_tables.stride(0)
+        a.kv_indptr = _ptr(kv_indptr)
+    a.block_tables = _ptr(block_tables)
+
+
+def tree_workspace_bytes(head_size: int) -> int:
+    """Bytes of :func:`paged_attention_tree`'s workspace on the current device."""
+    return int(lib().pkv_tree_workspace_bytes(int(head_size)))
+
+
+def paged_attention_tree(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                         value_cache: torch.Tensor, block_tables: torch.Tensor,
+                         seq_lens: torch.Tensor, cu_query_lens: torch.Tensor, scale: float, *,
+                         workspace: torch.Tensor, tree_mask: Optional[torch.Tensor] = None,
+                         positions: Optional[torch.Tensor] = None, logits_soft_cap: float = 0.0,
+                         kv_indptr: Optional[torch.Tensor] = None,
+                         err_flag: Optional[torch.Tensor] = None,
+                         max_blocks_per_seq: Optional[int] = None, kv_cache_dtype: str = "auto",
+                         k_scale: float = 1.0, v_scale: float = 1.0,
+                         alibi_slopes: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention of drafted tokens over the paged cache that already holds them.
+
+    ``query`` / ``out [num_tokens, num_heads, head_size]`` are the drafted tokens
+    of all sequences one behind the other (``cu_query_lens``, int32 ``[B + 1]``);
+    they are the last ones of ``seq_lens``.  A row sees every token before its
+    sequence's drafted ones, and drafted token j where ``tree_mask[row, j]`` (bool
+    or uint8, any strides) is set; without a mask, those up to itself.
+    ``logits_soft_cap`` > 0 caps the scaled scores by ``cap * tanh(z / cap)``;
+    ``alibi_slopes`` then adds ``slope * (pos(t) - pos(row))``, a drafted token's
+    position being ``positions[row]`` (int32) or its place in the sequence.
+    ``workspace``: ``tree_workspace_bytes(head_size)`` bytes, one for each call
+    that may run at the same time."""
+    _cuda(query, "query")
+    dev = _same_device(query, (out, "out"), (key_cache, "key_cache"), (value_cache, "value_cache"),
+                       (block_tables, "block_tables"), (seq_lens, "seq_lens"),
+                       (cu_query_lens, "cu_query_lens"), (workspace, "workspace"),
+                       (tree_mask, "tree_mask"), (positions, "positions"),
+                       (kv_indptr, "kv_indptr"), (err_flag, "err_flag"),
+                       (alibi_slopes, "alibi_slopes"))
+    if out.dtype != query.dtype or tuple(out.shape) != tuple(query.shape):
+        raise ValueError("out must match query's shape and dtype")
+    for t, n in ((cu_query_lens, "cu_query_lens"), (positions, "positions")):
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{n} must be int32")
+    a = _decode_args(query, key_cache, value_cache, block_tables, seq_lens, scale, kv_indptr,
+                     err_flag, max_blocks_per_seq, kv_cache_dtype, k_scale, v_scale, alibi_slopes)
+    n = query.shape[0]
+    a.num_seqs = seq_lens.numel()
+    _check_rows(seq_lens, "seq_lens", a.num_seqs)
+    _check_rows(cu_query_lens, "cu_query_lens", a.num_seqs + 1)
+    _check_rows(positions, "positions", n)
+    if tuple(value_cache.shape) != (key_cache.shape[0], key_cache.shape[1], query.shape[2],
+                                    key_cache.shape[3]) or \
+            key_cache.shape[2] * key_cache.shape[4] != query.shape[2]:
+        raise ValueError("query, key_cache and value_cache do not belong together")
+    _fill_tables(a, block_tables, kv_indptr, max_blocks_per_seq)
+    t = TreeArgs()
+    t.num_tokens = n
+    t.cu_query_lens, t.positions = _ptr(cu_query_lens), _ptr(positions)
+    if tree_mask is not None:
+        if tree_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("tree_mask must be bool or uint8")
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != n:
+            raise ValueError("tree_mask must be [num_tokens, columns]")
+        t.mask_cols = tree_mask.shape[1]
+        # a mask without columns hides every drafted token; its pointer may be null
+        t.tree_mask = _ptr(tree_mask) or _ptr(query)
+        _fill_strides(t.mask_stride, tree_mask)
+    t.logits_soft_cap = float(logits_soft_cap)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    t.workspace, t.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    os_ = _I64x3(*out.stride())
+    _call_on(dev, stream, "paged_attention_tree",
+             lambda s: lib().paged_attention_tree(_ptr(out), os_, ctypes.byref(a), ctypes.byref(t), s))

@@ -8,8 +8,10 @@
 
 #include "../../include/paged_kv.h"
 #include "attention_launch.cuh"
+#include "cache_io.cuh"
 #include "metadata.cuh"
 #include "reduce.cuh"
+#include "tree.cuh"
 
 namespace {
 
@@ -207,6 +209,46 @@ int pick_warps(const pkv_decode_args_t *a, int64_t units, Pass pass, int partiti
   return want;
 }
 
+// Checks shared by paged_kv_write and paged_kv_read: types, sizes and the cache layout.
+template <typename Args>
+pkv_status_t check_cache_args(const Args *a) {
+  const int tes = elem_size(a->dtype);
+  const bool fp8 = is_fp8_cache(a->kv_cache_dtype);
+  if (tes == 0 || (a->kv_cache_dtype != PKV_KV_AUTO && !fp8)) return PKV_ERR_INVALID_ARG;
+  if (fp8) {
+    if (!std::isfinite(a->k_scale) || !std::isfinite(a->v_scale)) return PKV_ERR_INVALID_ARG;
+    if (a->k_scale <= 0.f || a->v_scale <= 0.f) return PKV_ERR_INVALID_ARG;
+    if (a->dtype == PKV_F32) return PKV_ERR_UNSUPPORTED;
+  }
+  const int es = fp8 ? 1 : tes;
+  if (a->num_tokens < 0 || a->num_kv_heads < 1 || a->num_blocks < 1) return PKV_ERR_INVALID_ARG;
+  if (a->x * es != 16) return PKV_ERR_INVALID_ARG;
+  if (a->head_size < 1 || a->head_size % a->x != 0 || a->block_size < 1) return PKV_ERR_INVALID_ARG;
+  if (a->num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  if (smem_for(a->dtype, a->kv_cache_dtype, a->head_size, a->block_size, 1) == 0)
+    return PKV_ERR_UNSUPPORTED;
+  if (a->num_tokens == 0) return PKV_OK;
+  if (!a->key_cache || !a->value_cache) return PKV_ERR_INVALID_ARG;
+  const int64_t *ks = a->k_stride, *vs = a->v_stride;
+  if (ks[4] != 1 || ks[3] != a->x || ks[2] != int64_t(a->block_size) * a->x)
+    return PKV_ERR_UNSUPPORTED;
+  if (vs[3] != 1 || vs[2] != a->block_size) return PKV_ERR_UNSUPPORTED;
+  if (!aligned16(a->key_cache) || !aligned16(a->value_cache)) return PKV_ERR_INVALID_ARG;
+  if (!stride_bytes16(ks[0], es) || !stride_bytes16(ks[1], es) || !stride_bytes16(vs[0], es) ||
+      !stride_bytes16(vs[1], es))
+    return PKV_ERR_INVALID_ARG;
+  return PKV_OK;
+}
+
+// Token rows [num_tokens, num_kv_heads, head_size]: the elements of a head
+// must be adjacent; `vec` stays true while every row is on a 16-byte boundary.
+pkv_status_t check_token_rows(const void *p, const int64_t *stride, int es, bool &vec) {
+  if (!p || (reinterpret_cast<uintptr_t>(p) % unsigned(es)) != 0) return PKV_ERR_INVALID_ARG;
+  if (stride[2] != 1) return PKV_ERR_UNSUPPORTED;
+  vec = vec && aligned16(p) && stride_bytes16(stride[0], es) && stride_bytes16(stride[1], es);
+  return PKV_OK;
+}
+
 // fp8 caches of head size 128 / block size 16 run on the tensor-memory kernel
 // when it is selected (pkv_set_fp8_kernel(1)) and no warp count is forced (a
 // forced count names instances of the mma.sync kernel).
@@ -219,7 +261,7 @@ bool use_tensor_memory_kernel(const pkv_decode_args_t *a) {
 
 extern "C" {
 
-const char *pkv_version(void) { return "paged_kv 0.2.0 sm_103a"; }
+const char *pkv_version(void) { return "paged_kv 0.3.0 sm_103a"; }
 
 const char *pkv_status_string(pkv_status_t s) {
   switch (s) {
@@ -419,9 +461,172 @@ pkv_status_t prepare_decode_metadata(int32_t *page_indices, int64_t page_indices
                                      reinterpret_cast<cudaStream_t>(stream));
 }
 
+pkv_status_t paged_kv_write(const pkv_cache_write_args_t *a, pkv_stream_t stream) {
+  if (a == nullptr) return PKV_ERR_INVALID_ARG;
+  pkv_status_t st = check_cache_args(a);
+  if (st != PKV_OK) return st;
+  if (a->num_tokens == 0) return PKV_OK;
+  if (!a->slot_mapping) return PKV_ERR_INVALID_ARG;
+  bool vec = true;
+  const int es = elem_size(a->dtype);
+  if ((st = check_token_rows(a->key, a->key_stride, es, vec)) != PKV_OK) return st;
+  if ((st = check_token_rows(a->value, a->value_stride, es, vec)) != PKV_OK) return st;
+  pkv::CacheWriteParams p{};
+  p.key = a->key;
+  p.k_s0 = a->key_stride[0];
+  p.k_s1 = a->key_stride[1];
+  p.value = a->value;
+  p.v_s0 = a->value_stride[0];
+  p.v_s1 = a->value_stride[1];
+  p.key_cache = a->key_cache;
+  p.kc_s0 = a->k_stride[0];
+  p.kc_s1 = a->k_stride[1];
+  p.value_cache = a->value_cache;
+  p.vc_s0 = a->v_stride[0];
+  p.vc_s1 = a->v_stride[1];
+  p.slots = a->slot_mapping;
+  p.slot_stride = a->slot_stride;
+  p.num_slots = int64_t(a->num_blocks) * a->block_size;
+  p.err = a->err_flag;
+  p.num_tokens = a->num_tokens;
+  p.num_kv_heads = a->num_kv_heads;
+  p.head_size = a->head_size;
+  p.block_size = a->block_size;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  return pkv::launch_cache_write(p, a->dtype, a->kv_cache_dtype, vec,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+pkv_status_t paged_kv_read(const pkv_cache_read_args_t *a, pkv_stream_t stream) {
+  if (a == nullptr) return PKV_ERR_INVALID_ARG;
+  pkv_status_t st = check_cache_args(a);
+  if (st != PKV_OK) return st;
+  if (a->num_seqs < 0 || a->max_blocks_per_seq < 0) return PKV_ERR_INVALID_ARG;
+  if (a->num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+  if (a->num_tokens == 0 || a->num_seqs == 0) return PKV_OK;
+  if (!a->block_tables || !a->cu_seq_lens) return PKV_ERR_INVALID_ARG;
+  // a warp per (page, kv head), eight to a CTA
+  if ((int64_t(a->num_tokens) / a->block_size + 2 * int64_t(a->num_seqs)) * a->num_kv_heads / 8 >=
+      int64_t(0x7fffffff))
+    return PKV_ERR_UNSUPPORTED;
+  bool vec = true;
+  const int es = elem_size(a->dtype);
+  if ((st = check_token_rows(a->key_out, a->key_stride, es, vec)) != PKV_OK) return st;
+  if ((st = check_token_rows(a->value_out, a->value_stride, es, vec)) != PKV_OK) return st;
+  pkv::CacheReadParams p{};
+  p.key = a->key_out;
+  p.k_s0 = a->key_stride[0];
+  p.k_s1 = a->key_stride[1];
+  p.value = a->value_out;
+  p.v_s0 = a->value_stride[0];
+  p.v_s1 = a->value_stride[1];
+  p.key_cache = a->key_cache;
+  p.kc_s0 = a->k_stride[0];
+  p.kc_s1 = a->k_stride[1];
+  p.value_cache = a->value_cache;
+  p.vc_s0 = a->v_stride[0];
+  p.vc_s1 = a->v_stride[1];
+  p.bt = a->block_tables;
+  p.bt_s0 = a->bt_stride[0];
+  p.bt_s1 = a->bt_stride[1];
+  p.indptr = a->kv_indptr;
+  p.cu = a->cu_seq_lens;
+  p.starts = a->seq_starts;
+  p.err = a->err_flag;
+  p.num_seqs = a->num_seqs;
+  p.num_tokens = a->num_tokens;
+  p.num_kv_heads = a->num_kv_heads;
+  p.head_size = a->head_size;
+  p.block_size = a->block_size;
+  p.num_blocks = a->num_blocks;
+  p.max_blocks_per_seq = a->max_blocks_per_seq;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  return pkv::launch_cache_read(p, a->dtype, a->kv_cache_dtype, vec,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t pkv_cache_write_args_size(void) { return sizeof(pkv_cache_write_args_t); }
+size_t pkv_cache_read_args_size(void) { return sizeof(pkv_cache_read_args_t); }
+size_t pkv_tree_args_size(void) { return sizeof(pkv_tree_args_t); }
+size_t pkv_tree_workspace_bytes(int32_t head_size) { return pkv::tree_workspace_bytes(head_size); }
+
+pkv_status_t paged_attention_tree(void *out, const int64_t out_stride[3],
+                                  const pkv_decode_args_t *args, const pkv_tree_args_t *tree,
+                                  pkv_stream_t stream) {
+  if (!args || !tree || tree->num_tokens < 0 || tree->mask_cols < 0) return PKV_ERR_INVALID_ARG;
+  pkv_decode_args_t checked = *args;
+  if (tree->num_tokens == 0) checked.num_seqs = 0;  // no rows: nothing but the sizes matters
+  pkv_status_t st = check_decode_args(&checked);
+  if (st != PKV_OK) return st;
+  if (!std::isfinite(tree->logits_soft_cap) || tree->logits_soft_cap < 0.f)
+    return PKV_ERR_INVALID_ARG;
+  // row numbers of a sequence (drafted tokens x query heads of a kv head) are 32-bit
+  if (int64_t(tree->num_tokens) * (args->num_heads / args->num_kv_heads) > int64_t(0x7fff0000))
+    return PKV_ERR_UNSUPPORTED;
+  if (args->num_seqs == 0 || tree->num_tokens == 0) return PKV_OK;
+  if (!out || !out_stride || !tree->cu_query_lens || !tree->workspace) return PKV_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(tree->workspace) & 255u) != 0 ||
+      tree->workspace_bytes < pkv::tree_workspace_bytes(args->head_size))
+    return PKV_ERR_INVALID_ARG;
+  const bool fp8 = is_fp8_cache(args->kv_cache_dtype);
+  pkv::TreeParams p{};
+  p.q = args->query;
+  p.q_s0 = args->q_stride[0];
+  p.q_s1 = args->q_stride[1];
+  p.q_s2 = args->q_stride[2];
+  p.k = args->key_cache;
+  p.k_s0 = args->k_stride[0];
+  p.k_s1 = args->k_stride[1];
+  p.v = args->value_cache;
+  p.v_s0 = args->v_stride[0];
+  p.v_s1 = args->v_stride[1];
+  p.bt = args->block_tables;
+  p.bt_s0 = args->bt_stride[0];
+  p.bt_s1 = args->bt_stride[1];
+  p.indptr = args->kv_indptr;
+  p.seq_lens = args->seq_lens;
+  p.cu_q = tree->cu_query_lens;
+  p.mask = tree->tree_mask;
+  p.m_s0 = tree->mask_stride[0];
+  p.m_s1 = tree->mask_stride[1];
+  p.mask_cols = tree->mask_cols;
+  p.positions = tree->positions;
+  p.alibi = args->alibi_slopes;
+  p.err = args->err_flag;
+  p.out = out;
+  p.o_s0 = out_stride[0];
+  p.o_s1 = out_stride[1];
+  p.o_s2 = out_stride[2];
+  p.num_seqs = args->num_seqs;
+  p.num_tokens = tree->num_tokens;
+  p.num_heads = args->num_heads;
+  p.num_kv_heads = args->num_kv_heads;
+  p.group = args->num_heads / args->num_kv_heads;
+  p.num_blocks = args->num_blocks;
+  p.max_blocks_per_seq = args->max_blocks_per_seq;
+  p.block_size = args->block_size;
+  p.scale = fp8 ? args->scale * args->k_scale : args->scale;
+  p.cap = tree->logits_soft_cap;
+  p.out_scale = fp8 ? args->v_scale : 1.0f;
+  p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  p.extra_expect_tx = g_extra_expect_tx.exchange(0u, std::memory_order_relaxed);
+  return pkv::launch_tree_simt(args, p, tree->workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"
 
 namespace pkv {
+
+int tree_sm_count() { return sm_count(); }
+
+size_t tree_workspace_bytes(int head_size) {
+  const size_t ctas = size_t(sm_count()) * kTreeSimtCtasPerSm;
+  const size_t rows = 2 * ctas * kTreeSimtRows;
+  return (ctas * sizeof(TreeCut) + 255) / 256 * 256 +
+         rows * (sizeof(float2) + sizeof(float) * size_t(head_size > 0 ? head_size : 0));
+}
 
 pkv_status_t check_partition_args(const pkv_decode_args_t *args, int32_t max_num_partitions,
                                   int32_t partition_size, const int32_t *num_kv_splits) {

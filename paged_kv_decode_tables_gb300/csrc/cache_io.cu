@@ -1,0 +1,320 @@
+// Writing tokens into the paged caches (with quantisation to 8-bit codes) and
+// reading sequences back out of them.
+//
+// Both are copies with a change of layout, bounded by memory: a key chunk is
+// 16 bytes of one token in the cache, and a value page holds each head dim's
+// tokens next to one another, so values are transposed in 8 x 8 blocks (8
+// tokens x 8 dims) in registers, between 16-byte accesses on the token side
+// and 8-token runs on the cache side.
+//
+// Quantisation: code = the nearest code of the format to x / scale (an IEEE
+// fp32 division; ties to even, beyond the largest finite value: that value,
+// NaN stays NaN).  Reading back: code value * scale in fp32, rounded once to
+// the output's type.
+#include <type_traits>
+
+#include "cache_io.cuh"
+#include "pkv_launch.cuh"
+#include "pkv_ptx.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// N elements from p, in accesses of up to 16 bytes (`aligned`: p is on such a
+// boundary) or one by one.
+template <typename E, int N, bool ALIGNED>
+__device__ __forceinline__ void load_elems(const E *p, E (&v)[N]) {
+  constexpr int kBytes = N * int(sizeof(E));
+  if constexpr (ALIGNED && kBytes % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < kBytes / 16; ++i)
+      reinterpret_cast<uint4 *>(v)[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+  } else if constexpr (ALIGNED && kBytes % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < kBytes / 8; ++i)
+      reinterpret_cast<uint2 *>(v)[i] = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = p[i];
+  }
+}
+
+template <typename E, int N, bool ALIGNED>
+__device__ __forceinline__ void store_elems(E *p, const E (&v)[N]) {
+  constexpr int kBytes = N * int(sizeof(E));
+  if constexpr (ALIGNED && kBytes % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < kBytes / 16; ++i)
+      reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(v)[i];
+  } else if constexpr (ALIGNED && kBytes % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < kBytes / 8; ++i)
+      reinterpret_cast<uint2 *>(p)[i] = reinterpret_cast<const uint2 *>(v)[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = v[i];
+  }
+}
+
+// x / scale as a code of the cache (or x itself).
+template <typename T, typename KV>
+__device__ __forceinline__ KV to_cache(T x, float scale) {
+  if constexpr (is_fp8<KV>::value) {
+    const float q = __fdiv_rn(to_f32<T>(x), scale);
+    uint16_t r;
+    if constexpr (std::is_same<KV, fp8_e4m3_t>::value)
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(q));
+    else
+      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(q));
+    return KV{uint8_t(r)};
+  } else {
+    return x;
+  }
+}
+
+template <typename T, typename KV>
+__device__ __forceinline__ T from_cache(KV c, float scale) {
+  if constexpr (is_fp8<KV>::value) {
+    uint32_t lo, hi;
+    fp8x4_to_f16x2<KV>(c.bits, lo, hi);
+    return from_f32<T>(unpack2<__half>(lo).x * scale);
+  } else {
+    return c;
+  }
+}
+
+// ------------------------------------------------------------------- write --
+
+constexpr int kWTokens = 32;    // tokens of a CTA
+constexpr int kWThreads = 128;
+
+// CTA (x, h): tokens 32 x .. 32 x + 31 of kv head h.  Warp 0 cuts the tile into
+// groups of up to 8 consecutive slots that do not cross a multiple of 8; a
+// group of 8 is written 8 tokens at a time (a prompt), shorter ones token by
+// token (decode steps: every token goes to a page of its own).
+template <typename T, typename KV, bool VEC>
+__global__ void __launch_bounds__(kWThreads) cache_write_kernel(const CacheWriteParams p) {
+  constexpr int X = 16 / int(sizeof(KV));
+  __shared__ int64_t page_k[kWTokens], page_v[kWTokens];  // element offset of the token's page
+  __shared__ int slot_of[kWTokens];                       // slot in the page, -1: not written
+  __shared__ int group_first[kWTokens], group_size[kWTokens];
+  __shared__ int num_groups;
+  const int tid = threadIdx.x, D = p.head_size, BS = p.block_size, h = blockIdx.y;
+  const int64_t i0 = int64_t(blockIdx.x) * kWTokens;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if (tid < kWTokens) {
+    int64_t slot = -1;
+    if (i0 + tid < p.num_tokens) slot = p.slots[(i0 + tid) * p.slot_stride];
+    if (slot >= p.num_slots) {
+      flag_error(p.err, PKV_ERRF_BLOCK_ID);
+      slot = -1;
+    }
+    const int64_t blk = slot < 0 ? 0 : slot / BS;
+    page_k[tid] = blk * p.kc_s0 + int64_t(h) * p.kc_s1;
+    page_v[tid] = blk * p.vc_s0 + int64_t(h) * p.vc_s1;
+    slot_of[tid] = slot < 0 ? -1 : int(slot - blk * BS);
+    const int64_t prev = __shfl_up_sync(kFull, slot, 1);
+    const bool head = slot >= 0 && (tid == 0 || slot != prev + 1 || slot % 8 == 0 || prev < 0);
+    const unsigned heads = __ballot_sync(kFull, head);
+    const unsigned breaks = heads | __ballot_sync(kFull, slot < 0);
+    if (head) {
+      const int g = __popc(heads & ((1u << tid) - 1u));
+      const unsigned later = tid == 31 ? 0u : breaks >> (tid + 1);
+      group_first[g] = tid;
+      group_size[g] = later ? __ffs(later) : kWTokens - tid;
+    }
+    if (tid == 0) num_groups = __popc(heads);
+  }
+  __syncthreads();
+  const T *key = static_cast<const T *>(p.key) + int64_t(h) * p.k_s1;
+  const T *value = static_cast<const T *>(p.value) + int64_t(h) * p.v_s1;
+  KV *kc = static_cast<KV *>(p.key_cache), *vc = static_cast<KV *>(p.value_cache);
+  // keys: chunks of a token across lanes, so rows are read whole
+  const int chunks = D / X;
+  for (int i = tid; i < kWTokens * chunks; i += kWThreads) {
+    const int t = i / chunks, c = i - t * chunks;
+    if (slot_of[t] < 0) continue;
+    alignas(16) T x[X];
+    alignas(16) KV q[X];
+    load_elems<T, X, VEC>(key + (i0 + t) * p.k_s0 + c * X, x);
+#pragma unroll
+    for (int e = 0; e < X; ++e) q[e] = to_cache<T, KV>(x[e], p.k_scale);
+    store_elems<KV, X, true>(kc + page_k[t] + (int64_t(c) * BS + slot_of[t]) * X, q);
+  }
+  // values: (group, 8 dims) blocks
+  const int cols = D / 8;
+  const int ng = num_groups;
+  for (int i = tid; i < ng * cols; i += kWThreads) {
+    const int g = i / cols, d = (i - g * cols) * 8;
+    const int t0 = group_first[g], n = group_size[g];
+    KV *dst = vc + page_v[t0] + int64_t(d) * BS + slot_of[t0];
+    if (n == 8) {
+      alignas(16) KV b[8][8];  // [dim][token]
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        alignas(16) T x[8];
+        load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[e][t] = to_cache<T, KV>(x[e], p.v_scale);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) store_elems<KV, 8, true>(dst + e * BS, b[e]);
+    } else {
+      for (int t = 0; t < n; ++t) {
+        alignas(16) T x[8];
+        load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dst[e * BS + t] = to_cache<T, KV>(x[e], p.v_scale);
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------------- read --
+
+constexpr int kRThreads = 256;
+
+// A warp per (page of a sequence, kv head).  The pages of all sequences are
+// numbered without a scan of their counts: sequence s takes the numbers from
+// cu[s] / BS + 2 s on, which leaves it at least as many as the pages that its
+// tokens touch (a few numbers stay unused); the warp finds s by a search with
+// 32 probes a step.
+template <typename T, typename KV, bool VEC>
+__global__ void __launch_bounds__(kRThreads) cache_read_kernel(const CacheReadParams p) {
+  constexpr int X = 16 / int(sizeof(KV));
+  const int lane = threadIdx.x & 31, D = p.head_size, BS = p.block_size;
+  const int64_t w = int64_t(blockIdx.x) * (kRThreads / 32) + (threadIdx.x >> 5);
+  const int64_t u = w / p.num_kv_heads;
+  const int h = int(w - u * p.num_kv_heads);
+  grid_dependency_wait();
+  allow_dependent_launch();
+  // the last s with cu[s] / BS + 2 s <= u
+  int lo = 0, hi = p.num_seqs;  // s is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int s = lo + lane * step;
+    const bool le = s < hi && (s == lo || max(p.cu[s], 0) / BS + 2 * int64_t(s) <= u);
+    const unsigned b = __ballot_sync(kFull, le);
+    const int last = 31 - __clz(int(b));  // lane 0 is always set
+    lo += last * step;
+    hi = min(hi, lo + step);
+  }
+  const int s = lo;
+  const int c0 = p.cu[s], c1 = p.cu[s + 1];
+  const int first = p.starts ? p.starts[s] : 0;
+  int64_t row = int64_t(s) * p.bt_s0, cap = p.max_blocks_per_seq;
+  if (p.indptr) {
+    const int a = p.indptr[s];
+    row = int64_t(max(a, 0)) * p.bt_s1;
+    cap = a < 0 ? 0 : int64_t(p.indptr[s + 1]) - a;
+  }
+  if (c0 < 0 || c1 < c0 || c1 > p.num_tokens || cap < 0) {
+    if (lane == 0) flag_error(p.err, PKV_ERRF_INDPTR);
+    return;
+  }
+  if (first < 0 || int64_t(first) + (c1 - c0) > cap * BS) {
+    if (lane == 0 && c1 > c0) flag_error(p.err, PKV_ERRF_SEQ_LEN);
+    if (first < 0) return;
+  }
+  const int64_t page = first / BS + (u - (c0 / BS + 2 * int64_t(s)));
+  // tokens [t0, t1) of the sequence stand in this page
+  const int64_t t0 = max(page * BS, int64_t(first));
+  const int64_t t1 = min((page + 1) * BS, int64_t(first) + (c1 - c0));
+  if (t0 >= t1 || page >= cap) return;
+  int blk = p.bt[row + page * p.bt_s1];
+  if (blk < 0 || blk >= p.num_blocks) {
+    if (lane == 0) flag_error(p.err, PKV_ERRF_BLOCK_ID);
+    blk = 0;
+  }
+  const int a = int(t0 - page * BS), b = int(t1 - page * BS);  // slots [a, b)
+  const int64_t out0 = c0 + (page * BS - first);               // output row of slot 0
+  const KV *kc = static_cast<const KV *>(p.key_cache) + int64_t(blk) * p.kc_s0 + int64_t(h) * p.kc_s1;
+  const KV *vc = static_cast<const KV *>(p.value_cache) + int64_t(blk) * p.vc_s0 + int64_t(h) * p.vc_s1;
+  T *key = static_cast<T *>(p.key) + out0 * p.k_s0 + int64_t(h) * p.k_s1;
+  T *value = static_cast<T *>(p.value) + out0 * p.v_s0 + int64_t(h) * p.v_s1;
+  const int chunks = D / X;
+  for (int i = lane; i < chunks * BS; i += 32) {
+    const int t = i / chunks, c = i - t * chunks;
+    if (t < a || t >= b) continue;
+    alignas(16) KV q[X];
+    alignas(16) T x[X];
+    load_elems<KV, X, true>(kc + (c * BS + t) * X, q);
+#pragma unroll
+    for (int e = 0; e < X; ++e) x[e] = from_cache<T, KV>(q[e], p.k_scale);
+    store_elems<T, X, VEC>(key + int64_t(t) * p.k_s0 + c * X, x);
+  }
+  // blocks of 8 tokens x 8 dims, the page's token groups next to one another
+  const int groups = BS / 8;
+  for (int i = lane; i < groups * (D / 8); i += 32) {
+    const int g = i % groups, d = i / groups * 8;
+    alignas(16) KV q[8][8];  // [dim][token]
+#pragma unroll
+    for (int e = 0; e < 8; ++e) load_elems<KV, 8, true>(vc + (d + e) * BS + g * 8, q[e]);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      if (g * 8 + t < a || g * 8 + t >= b) continue;
+      alignas(16) T x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = from_cache<T, KV>(q[e][t], p.v_scale);
+      store_elems<T, 8, VEC>(value + int64_t(g * 8 + t) * p.v_s0 + d, x);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launch --
+
+template <typename T, typename KV>
+cudaError_t write_as(const CacheWriteParams &p, bool vec, cudaStream_t s) {
+  const dim3 grid((int64_t(p.num_tokens) + kWTokens - 1) / kWTokens, p.num_kv_heads);
+  if (vec)
+    return launch_programmatic(cache_write_kernel<T, KV, true>, grid, dim3(kWThreads), 0, s, p);
+  return launch_programmatic(cache_write_kernel<T, KV, false>, grid, dim3(kWThreads), 0, s, p);
+}
+
+template <typename T, typename KV>
+cudaError_t read_as(const CacheReadParams &p, bool vec, cudaStream_t s) {
+  const int64_t pages = p.num_tokens / p.block_size + 2 * int64_t(p.num_seqs);
+  const int64_t warps = pages * p.num_kv_heads;
+  const dim3 grid((warps + kRThreads / 32 - 1) / (kRThreads / 32));
+  if (vec) return launch_programmatic(cache_read_kernel<T, KV, true>, grid, dim3(kRThreads), 0, s, p);
+  return launch_programmatic(cache_read_kernel<T, KV, false>, grid, dim3(kRThreads), 0, s, p);
+}
+
+// F(T, KV) for the element types of (dtype, kv); F returns a cudaError_t.
+template <typename F>
+pkv_status_t dispatch(pkv_dtype_t dtype, int32_t kv, F &&f) {
+  cudaError_t e;
+  const int k = kv == PKV_KV_AUTO ? 0 : (kv == PKV_KV_FP8_E4M3 ? 1 : 2);
+  if (dtype == PKV_F32 && k == 0)
+    e = f(float(), float());
+  else if (dtype == PKV_F16)
+    e = k == 0 ? f(__half(), __half()) : (k == 1 ? f(__half(), fp8_e4m3_t()) : f(__half(), fp8_e5m2_t()));
+  else if (dtype == PKV_BF16)
+    e = k == 0 ? f(__nv_bfloat16(), __nv_bfloat16())
+               : (k == 1 ? f(__nv_bfloat16(), fp8_e4m3_t()) : f(__nv_bfloat16(), fp8_e5m2_t()));
+  else
+    return PKV_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+pkv_status_t launch_cache_write(const CacheWriteParams &p, pkv_dtype_t dtype, int32_t kv, bool vec,
+                                cudaStream_t stream) {
+  return dispatch(dtype, kv, [&](auto t, auto c) {
+    return write_as<decltype(t), decltype(c)>(p, vec, stream);
+  });
+}
+
+pkv_status_t launch_cache_read(const CacheReadParams &p, pkv_dtype_t dtype, int32_t kv, bool vec,
+                               cudaStream_t stream) {
+  return dispatch(dtype, kv, [&](auto t, auto c) {
+    return read_as<decltype(t), decltype(c)>(p, vec, stream);
+  });
+}
+
+}  // namespace pkv

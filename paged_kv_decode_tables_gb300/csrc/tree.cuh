@@ -1,0 +1,302 @@
+// Attention of drafted token trees over a paged cache: what its kernels share.
+//
+// Rows.  Sequence s has T_s drafted tokens (cu_query_lens), the last T_s of
+// its seq_lens[s] cached tokens.  A kv head serves T_s * group query rows; row
+// R is drafted token R / group under query head R % group of the kv head's
+// group.  Rows are taken RT at a time (a row tile).
+//
+// Units and split.  A unit is (sequence, kv head, row tile); its work is its
+// sequence's tiles of TT tokens (at least one).  All units' tiles, laid end to
+// end, are cut into equal runs, one per CTA, whatever the lengths are: a batch
+// of uneven sequences and a single long one both fill the GPU, and the
+// partial results are bounded by two per CTA (a run's first and last unit) --
+// the workspace depends on the GPU and the head size only.  A unit inside one
+// run is written to `out` by its CTA; the others are joined by
+// tree_join_kernel from their partial sums (acc = sum 2^(x - m) v, l = sum
+// 2^(x - m), m; x in log2 units).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/paged_kv.h"
+#include "pkv_ptx.cuh"
+
+namespace pkv {
+
+// A unit cut between CTAs, as the CTA whose run starts first inside it
+// describes it for the join.
+struct TreeCut {
+  int32_t valid;
+  int32_t q0, rows, kvh, row0;  // first query row, rows of the (sequence, kv head), row tile
+  int32_t parts;                // CTAs of the split grid
+  int64_t begin, end, total;    // the unit's tiles among all `total`
+};
+
+struct TreeParams {
+  const void *q;
+  int64_t q_s0, q_s1, q_s2;
+  const void *k;
+  int64_t k_s0, k_s1;
+  const void *v;
+  int64_t v_s0, v_s1;
+  const int32_t *bt;
+  int64_t bt_s0, bt_s1;
+  const int32_t *indptr;
+  const int32_t *seq_lens;
+  const int32_t *cu_q;       // [num_seqs + 1]
+  const uint8_t *mask;       // [num_tokens, mask_cols], or null (a chain)
+  int64_t m_s0, m_s1;
+  const int32_t *positions;  // [num_tokens], or null (place in the sequence)
+  const float *alibi;        // [num_heads], or null
+  int32_t *err;
+  void *out;
+  int64_t o_s0, o_s1, o_s2;
+  TreeCut *cuts;  // workspace: [CTAs]
+  float2 *ml;     // workspace: [2 * CTAs][RT] (m, l)
+  float *acc;     // workspace: [2 * CTAs][RT][D]
+  int32_t num_seqs, num_tokens, num_heads, num_kv_heads, group, num_blocks, max_blocks_per_seq;
+  int32_t block_size, mask_cols;
+  float scale;      // of the score: args->scale (x k_scale for fp8 caches)
+  float cap;        // logits_soft_cap, or 0
+  float out_scale;  // v_scale for fp8 caches, else 1
+  uint64_t wait_limit_ns;
+  uint32_t extra_expect_tx;
+};
+
+// What the kernels need of one sequence.  Bad device data (negative or
+// descending cu_query_lens, rows past num_tokens, lengths past the table or
+// shorter than the drafted tokens) is clamped, and flagged where `flag`.
+struct TreeSeq {
+  int32_t q0, T, L, ctx;  // first query row, drafted tokens, tokens, tokens before the drafted
+  int32_t tiles, row_tiles;
+};
+
+template <int TT, int RT>
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s, bool flag) {
+  TreeSeq r;
+  int L = p.seq_lens[s];
+  const int q0 = p.cu_q[s], q1 = p.cu_q[s + 1];
+  int64_t cap_pages = p.max_blocks_per_seq;
+  if (p.indptr != nullptr) {
+    const int a = p.indptr[s], b = p.indptr[s + 1];
+    cap_pages = int64_t(b) - a;
+    if (a < 0 || cap_pages < 0) {
+      if (flag) flag_error(p.err, PKV_ERRF_INDPTR);
+      cap_pages = 0;
+    }
+  }
+  if (L < 0 || int64_t(L) > cap_pages * p.block_size) {
+    if (flag) flag_error(p.err, PKV_ERRF_SEQ_LEN);
+    L = L < 0 ? 0 : int(cap_pages * p.block_size);
+  }
+  int T = 0;
+  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens) {
+    if (flag) flag_error(p.err, PKV_ERRF_INDPTR);
+  } else {
+    T = q1 - q0;
+  }
+  if (T > L) {
+    // rows without a cached token of their own: only the first L are drafted
+    // tokens of the cache, all rows are computed over those
+    if (flag) flag_error(p.err, PKV_ERRF_SEQ_LEN);
+  }
+  r.q0 = q0;
+  r.T = T;
+  r.L = L;
+  r.ctx = L > T ? L - T : 0;
+  r.tiles = L > 0 ? int((unsigned(L) + (TT - 1)) / TT) : 1;
+  r.row_tiles = int((int64_t(T) * p.group + (RT - 1)) / RT);
+  return r;
+}
+
+__device__ __forceinline__ int64_t tree_weight(const TreeParams &p, const TreeSeq &q) {
+  return int64_t(q.row_tiles) * p.num_kv_heads * q.tiles;
+}
+
+// Block-table row of sequence s (its page j: bt[row + j * bt_s1]).
+__device__ __forceinline__ int64_t tree_table_row(const TreeParams &p, int s) {
+  if (p.indptr == nullptr) return int64_t(s) * p.bt_s0;
+  const int a = p.indptr[s];
+  return int64_t(a < 0 ? 0 : a) * p.bt_s1;
+}
+
+// Block id of a sequence's page (an id out of range is flagged and read as
+// block 0).
+__device__ __forceinline__ int tree_block_id(const TreeParams &p, int64_t row, int64_t page) {
+  int id = __ldg(p.bt + row + page * p.bt_s1);
+  if (id < 0 || id >= p.num_blocks) {
+    flag_error(p.err, PKV_ERRF_BLOCK_ID);
+    id = 0;
+  }
+  return id;
+}
+
+// Where CTA `c` of `parts` starts among `total` tiles.
+__host__ __device__ __forceinline__ int64_t tree_start(int64_t total, int c, int parts) {
+  return total / parts * c + total % parts * c / parts;
+}
+
+// A CTA's place in the work: its run [begin, end) of tiles and the sequence
+// that `begin` falls into (`base`: that sequence's first tile).
+struct TreeRun {
+  int64_t total, begin, end, base;
+  int32_t seq, parts;
+};
+
+// Sums the batch's tiles over the CTA's NT threads and finds the run of CTA
+// blockIdx.x.  Every thread returns the same run; begin == end: nothing to do.
+// `scratch`: NT / 32 + 3 words of shared memory, free again after the call's
+// last barrier has been passed by a later __syncthreads().
+template <int TT, int RT, int NT>
+__device__ __forceinline__ TreeRun tree_find_run(const TreeParams &p, int64_t *scratch) {
+  constexpr int NW = NT / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.num_seqs + NT - 1) / NT;
+  const int s0 = min(int64_t(tid) * per, int64_t(p.num_seqs));
+  const int s1 = min(s0 + per, p.num_seqs);
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s)
+    mine += tree_weight(p, tree_seq<TT, RT>(p, s, blockIdx.x == 0));
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const int64_t t = scratch[w];
+    if (w < warp) before += t;
+    total += t;
+  }
+  TreeRun r;
+  r.total = total;
+  r.parts = int(min(int64_t(gridDim.x), total));
+  r.begin = r.end = 0;
+  r.base = 0;
+  r.seq = 0;
+  if (int(blockIdx.x) >= r.parts) return r;  // the same for every thread
+  r.begin = tree_start(total, blockIdx.x, r.parts);
+  r.end = tree_start(total, blockIdx.x + 1, r.parts);
+  const int64_t first = before + incl - mine;
+  if (r.begin >= first && r.begin < first + mine) {
+    int64_t at = first;
+    for (int s = s0; s < s1; ++s) {
+      const int64_t w = tree_weight(p, tree_seq<TT, RT>(p, s, false));
+      if (r.begin < at + w) {
+        scratch[NW] = s;
+        scratch[NW + 1] = at;
+        break;
+      }
+      at += w;
+    }
+  }
+  __syncthreads();
+  r.seq = int(scratch[NW]);
+  r.base = scratch[NW + 1];
+  return r;
+}
+
+// One stretch of tiles of one unit within a CTA's run.
+struct TreeStretch {
+  int32_t seq, kvh, row0, rows;  // rows: valid rows from row0 on, at most RT
+  int32_t tile0, tile1, tiles;
+  TreeSeq q;
+};
+
+// Steps through a run stretch by stretch (one thread, or threads in step).
+template <int TT, int RT>
+struct TreeWalk {
+  TreeRun run;
+  int64_t pos, base;
+  int32_t seq;
+  TreeSeq q;
+  bool fresh;
+
+  __device__ __forceinline__ void start(const TreeParams &p, const TreeRun &r) {
+    run = r;
+    pos = r.begin;
+    base = r.base;
+    seq = r.seq;
+    q = tree_seq<TT, RT>(p, seq, false);
+  }
+  __device__ __forceinline__ bool next(const TreeParams &p, TreeStretch &s) {
+    if (pos >= run.end) return false;
+    int64_t w;
+    while (pos >= base + (w = tree_weight(p, q))) {
+      base += w;
+      ++seq;
+      q = tree_seq<TT, RT>(p, seq, false);
+    }
+    const int64_t off = pos - base;
+    const int64_t u = off / q.tiles;
+    s.seq = seq;
+    s.q = q;
+    s.kvh = int(u / q.row_tiles);
+    s.row0 = int(u - int64_t(s.kvh) * q.row_tiles) * RT;
+    s.rows = int(min(int64_t(RT), int64_t(q.T) * p.group - s.row0));
+    s.tile0 = int(off - u * q.tiles);
+    s.tile1 = int(min(int64_t(q.tiles), s.tile0 + (run.end - pos)));
+    s.tiles = q.tiles;
+    pos += s.tile1 - s.tile0;
+    return true;
+  }
+};
+
+// Describes the unit that CTA blockIdx.x's run starts inside of, for the
+// join; one thread.  `s` is the run's first stretch (null: an empty run).
+__device__ __forceinline__ void tree_write_cut(const TreeParams &p, const TreeRun &r,
+                                               const TreeStretch *s) {
+  TreeCut c = {};
+  if (s != nullptr && s->tile0 > 0) {
+    c.begin = r.begin - s->tile0;
+    c.end = c.begin + s->tiles;
+    // the first run that starts inside the unit describes it
+    c.valid = tree_start(r.total, int(blockIdx.x) - 1, r.parts) <= c.begin;
+    c.q0 = s->q.q0;
+    c.rows = s->rows;
+    c.kvh = s->kvh;
+    c.row0 = s->row0;
+    c.parts = r.parts;
+    c.total = r.total;
+  }
+  p.cuts[blockIdx.x] = c;
+}
+
+// log2(e) * logit of a score `d` (the dot product): scaled, capped, biased.
+// CAP: cap * tanh(z / cap) as cap - 2 cap / (1 + e^(2 z / cap)), which is
+// exact to about 3e-7 * cap (ex2 and the reciprocal are good to 2^-22);
+// EXACT_TANH: with tanhf, for fp32 outputs.
+struct TreeLogit {
+  float scale_log2, cap_log2, cap_arg;
+  __device__ __forceinline__ explicit TreeLogit(const TreeParams &p) {
+    constexpr float kLog2E = 1.44269504088896340736f;
+    scale_log2 = p.scale * kLog2E;
+    cap_log2 = p.cap * kLog2E;
+    cap_arg = p.cap > 0.f ? p.scale / p.cap : 0.f;
+  }
+  __device__ __forceinline__ float plain(float d) const { return d * scale_log2; }
+  __device__ __forceinline__ float capped_exact(float d) const {
+    return cap_log2 * tanhf(d * cap_arg);
+  }
+  __device__ __forceinline__ float capped(float d) const {
+    const float e = ex2(d * (cap_arg * 2.88539008177792681472f));
+    return fmaf(-2.f * cap_log2, __frcp_rn(1.f + e), cap_log2);
+  }
+};
+
+// CTAs of the split grid and rows of a row tile, per kernel (the workspace
+// holds the larger).
+constexpr int kTreeSimtRows = 32, kTreeSimtTokens = 64, kTreeSimtCtasPerSm = 2;
+
+size_t tree_workspace_bytes(int head_size);
+pkv_status_t launch_tree_simt(const pkv_decode_args_t *args, TreeParams &p, void *workspace,
+                              cudaStream_t stream);
+pkv_status_t launch_tree_join(const TreeParams &p, pkv_dtype_t dtype, int head_size, int rows,
+                              int ctas, cudaStream_t stream);
+int tree_sm_count();
+
+}  // namespace pkv
