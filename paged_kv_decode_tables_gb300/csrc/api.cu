@@ -249,6 +249,30 @@ pkv_status_t check_token_rows(const void *p, const int64_t *stride, int es, bool
   return PKV_OK;
 }
 
+// paged_attention_tree's grid and where the parts of its workspace start: the
+// cuts, then (m, l) and the sums of two partial results per CTA.
+struct TreeWorkspace {
+  int ctas, rows;
+  size_t ml, acc, bytes;
+};
+
+TreeWorkspace tree_workspace(bool fp32, int head_size) {
+  TreeWorkspace w;
+  w.ctas = sm_count() * (fp32 ? pkv::kTreeSimtCtasPerSm : 1);
+  w.rows = fp32 ? pkv::kTreeSimtRows : pkv::kTreeTcRows;
+  w.ml = (size_t(w.ctas) * sizeof(pkv::TreeCut) + 255) / 256 * 256;
+  const size_t rows = size_t(2) * w.ctas * w.rows;
+  w.acc = w.ml + rows * sizeof(float2);
+  w.bytes = w.acc + rows * sizeof(float) * size_t(head_size > 0 ? head_size : 0);
+  return w;
+}
+
+// Enough for every query type.
+size_t tree_workspace_bytes(int head_size) {
+  const size_t a = tree_workspace(false, head_size).bytes, b = tree_workspace(true, head_size).bytes;
+  return a > b ? a : b;
+}
+
 // fp8 caches of head size 128 / block size 16 run on the tensor-memory kernel
 // when it is selected (pkv_set_fp8_kernel(1)) and no warp count is forced (a
 // forced count names instances of the mma.sync kernel).
@@ -550,7 +574,7 @@ pkv_status_t paged_kv_read(const pkv_cache_read_args_t *a, pkv_stream_t stream) 
 size_t pkv_cache_write_args_size(void) { return sizeof(pkv_cache_write_args_t); }
 size_t pkv_cache_read_args_size(void) { return sizeof(pkv_cache_read_args_t); }
 size_t pkv_tree_args_size(void) { return sizeof(pkv_tree_args_t); }
-size_t pkv_tree_workspace_bytes(int32_t head_size) { return pkv::tree_workspace_bytes(head_size); }
+size_t pkv_tree_workspace_bytes(int32_t head_size) { return tree_workspace_bytes(head_size); }
 
 pkv_status_t paged_attention_tree(void *out, const int64_t out_stride[3],
                                   const pkv_decode_args_t *args, const pkv_tree_args_t *tree,
@@ -568,7 +592,7 @@ pkv_status_t paged_attention_tree(void *out, const int64_t out_stride[3],
   if (args->num_seqs == 0 || tree->num_tokens == 0) return PKV_OK;
   if (!out || !out_stride || !tree->cu_query_lens || !tree->workspace) return PKV_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(tree->workspace) & 255u) != 0 ||
-      tree->workspace_bytes < pkv::tree_workspace_bytes(args->head_size))
+      tree->workspace_bytes < tree_workspace_bytes(args->head_size))
     return PKV_ERR_INVALID_ARG;
   const bool fp8 = is_fp8_cache(args->kv_cache_dtype);
   pkv::TreeParams p{};
@@ -612,21 +636,31 @@ pkv_status_t paged_attention_tree(void *out, const int64_t out_stride[3],
   p.out_scale = fp8 ? args->v_scale : 1.0f;
   p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   p.extra_expect_tx = g_extra_expect_tx.exchange(0u, std::memory_order_relaxed);
-  return pkv::launch_tree_simt(args, p, tree->workspace, reinterpret_cast<cudaStream_t>(stream));
+  const TreeWorkspace w = tree_workspace(args->dtype == PKV_F32, args->head_size);
+  uint8_t *base = static_cast<uint8_t *>(tree->workspace);
+  p.cuts = reinterpret_cast<pkv::TreeCut *>(base);
+  p.ml = reinterpret_cast<float2 *>(base + w.ml);
+  p.acc = reinterpret_cast<float *>(base + w.acc);
+  const int D = args->head_size;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool e4m3 = args->kv_cache_dtype == PKV_KV_FP8_E4M3;
+  if (args->dtype == PKV_F32)
+    st = pkv::launch_tree_simt(p, D, w.ctas, s);
+  else if (args->dtype == PKV_F16)
+    st = !fp8 ? pkv::launch_tree_tc_f16(p, D, w.ctas, s)
+              : (e4m3 ? pkv::launch_tree_tc_f16_e4m3(p, D, w.ctas, s)
+                      : pkv::launch_tree_tc_f16_e5m2(p, D, w.ctas, s));
+  else
+    st = !fp8 ? pkv::launch_tree_tc_bf16(p, D, w.ctas, s)
+              : (e4m3 ? pkv::launch_tree_tc_bf16_e4m3(p, D, w.ctas, s)
+                      : pkv::launch_tree_tc_bf16_e5m2(p, D, w.ctas, s));
+  if (st != PKV_OK) return st;
+  return pkv::launch_tree_join(p, args->dtype, D, w.rows, w.ctas, s);
 }
 
 }  // extern "C"
 
 namespace pkv {
-
-int tree_sm_count() { return sm_count(); }
-
-size_t tree_workspace_bytes(int head_size) {
-  const size_t ctas = size_t(sm_count()) * kTreeSimtCtasPerSm;
-  const size_t rows = 2 * ctas * kTreeSimtRows;
-  return (ctas * sizeof(TreeCut) + 255) / 256 * 256 +
-         rows * (sizeof(float2) + sizeof(float) * size_t(head_size > 0 ? head_size : 0));
-}
 
 pkv_status_t check_partition_args(const pkv_decode_args_t *args, int32_t max_num_partitions,
                                   int32_t partition_size, const int32_t *num_kv_splits) {

@@ -267,9 +267,9 @@ __device__ __forceinline__ void tree_write_cut(const TreeParams &p, const TreeRu
 }
 
 // log2(e) * logit of a score `d` (the dot product): scaled, capped, biased.
-// CAP: cap * tanh(z / cap) as cap - 2 cap / (1 + e^(2 z / cap)), which is
+// capped: cap * tanh(z / cap) as cap - 2 cap / (1 + e^(2 z / cap)), which is
 // exact to about 3e-7 * cap (ex2 and the reciprocal are good to 2^-22);
-// EXACT_TANH: with tanhf, for fp32 outputs.
+// capped_exact: with tanhf, for fp32 outputs.
 struct TreeLogit {
   float scale_log2, cap_log2, cap_arg;
   __device__ __forceinline__ explicit TreeLogit(const TreeParams &p) {
@@ -288,15 +288,21 @@ struct TreeLogit {
   }
 };
 
-// CTAs of the split grid and rows of a row tile, per kernel (the workspace
-// holds the larger).
+// The fp32 kernel's row tile, token tile and CTAs per SM, and the tensor-core
+// kernel's rows (one CTA per SM).
 constexpr int kTreeSimtRows = 32, kTreeSimtTokens = 64, kTreeSimtCtasPerSm = 2;
+constexpr int kTreeTcRows = 128;
 
-size_t tree_workspace_bytes(int head_size);
-pkv_status_t launch_tree_simt(const pkv_decode_args_t *args, TreeParams &p, void *workspace,
-                              cudaStream_t stream);
+pkv_status_t launch_tree_simt(const TreeParams &p, int head_size, int ctas, cudaStream_t stream);
+// Queries and caches of 16 bits, and 16-bit queries over 8-bit caches.
+pkv_status_t launch_tree_tc_f16(const TreeParams &p, int head_size, int ctas, cudaStream_t s);
+pkv_status_t launch_tree_tc_bf16(const TreeParams &p, int head_size, int ctas, cudaStream_t s);
+pkv_status_t launch_tree_tc_f16_e4m3(const TreeParams &p, int head_size, int ctas, cudaStream_t s);
+pkv_status_t launch_tree_tc_f16_e5m2(const TreeParams &p, int head_size, int ctas, cudaStream_t s);
+pkv_status_t launch_tree_tc_bf16_e4m3(const TreeParams &p, int head_size, int ctas, cudaStream_t s);
+pkv_status_t launch_tree_tc_bf16_e5m2(const TreeParams &p, int head_size, int ctas, cudaStream_t s);
+// `rows`: the kernel's row tile, `ctas`: its grid.
 pkv_status_t launch_tree_join(const TreeParams &p, pkv_dtype_t dtype, int head_size, int rows,
                               int ctas, cudaStream_t stream);
-int tree_sm_count();
 
 }  // namespace pkv

@@ -1,9 +1,8 @@
-// Tree attention, plain kernel: fp32 arithmetic on the CUDA cores, any query
-// type and cache format (the split, the masks and the join are described in
-// tree.cuh).
+// Tree attention in fp32, on the CUDA cores (the split, the masks and the join
+// are described in tree.cuh).
 //
 // One CTA of 128 threads takes 32 query rows against tiles of 64 tokens: the
-// tile's keys are widened to fp32 in shared memory, thread (rg, tg) computes
+// tile's keys go to shared memory token by token, thread (rg, tg) computes
 // the scores of rows 4 rg .. 4 rg + 3 with tokens tg, tg + 16, ..., the
 // online softmax runs over the 16 lanes that share rows, and after the tile's
 // values have replaced its keys the thread adds its rows' products for dims
@@ -22,40 +21,17 @@ namespace {
 
 constexpr int kRT = kTreeSimtRows, kTT = kTreeSimtTokens, kThreads = 128;
 
-template <typename T, typename KV, int D>
+template <int D>
 struct SimtCfg {
   static constexpr int kPitch = D + 4;  // floats; spreads the rows of a column over the banks
   static constexpr int kSmem = (kRT * kPitch + kTT * kPitch + kRT * (kTT + 4)) * 4;
 };
 
-template <typename KV, int N>
-__device__ __forceinline__ void widen(const uint8_t *src, float (&f)[N]) {
-  if constexpr (is_fp8<KV>::value) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      uint32_t lo, hi;
-      fp8x4_to_f16x2<KV>(reinterpret_cast<const uint32_t *>(src)[i], lo, hi);
-      const float2 a = unpack2<__half>(lo), b = unpack2<__half>(hi);
-      f[4 * i] = a.x;
-      f[4 * i + 1] = a.y;
-      f[4 * i + 2] = b.x;
-      f[4 * i + 3] = b.y;
-    }
-  } else {
-    const KV *s = reinterpret_cast<const KV *>(src);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = to_f32<KV>(s[i]);
-  }
-}
-
-template <typename T, typename KV, int D, int BS>
+template <int D, int BS>
 __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel(const TreeParams p) {
-  using Cfg = SimtCfg<T, KV, D>;
-  constexpr int CS = int(sizeof(KV));
-  constexpr int X = 16 / CS;                     // elements of a key chunk
-  constexpr int VT = BS * CS >= 16 ? X : BS;     // tokens of a value load
+  using Cfg = SimtCfg<D>;
+  constexpr int X = 4;  // elements of 16 bytes: a key chunk's dims, a value load's tokens
   constexpr int kPitch = Cfg::kPitch, kPP = kTT + 4;
-  constexpr bool kExact = std::is_same<T, float>::value;
   extern __shared__ __align__(16) float tree_simt_smem[];
   float *qs = tree_simt_smem;
   float *kv = qs + kRT * kPitch;
@@ -84,9 +60,9 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
       const int r = i / D, d = i % D, R = st.row0 + r;
       float x = 0.f;
       if (r < st.rows)
-        x = to_f32<T>(static_cast<const T *>(p.q)[int64_t(st.q.q0 + R / p.group) * p.q_s0 +
-                                                  int64_t(st.kvh * p.group + R % p.group) * p.q_s1 +
-                                                  int64_t(d) * p.q_s2]);
+        x = static_cast<const float *>(p.q)[int64_t(st.q.q0 + R / p.group) * p.q_s0 +
+                                            int64_t(st.kvh * p.group + R % p.group) * p.q_s1 +
+                                            int64_t(d) * p.q_s2];
       qs[r * kPitch + d] = x;
     }
     int node[4];
@@ -108,8 +84,8 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
       for (int e = 0; e < D / 16; ++e) acc[i][e] = 0.f;
     }
     const int64_t row = tree_table_row(p, st.seq);
-    const uint8_t *kb = static_cast<const uint8_t *>(p.k) + int64_t(st.kvh) * p.k_s1 * CS;
-    const uint8_t *vb = static_cast<const uint8_t *>(p.v) + int64_t(st.kvh) * p.v_s1 * CS;
+    const float *kb = static_cast<const float *>(p.k) + int64_t(st.kvh) * p.k_s1;
+    const float *vb = static_cast<const float *>(p.v) + int64_t(st.kvh) * p.v_s1;
     for (int tile = st.tile0; tile < st.tile1; ++tile) {
       const int t0 = tile * kTT, n = min(kTT, st.q.L - t0);  // n <= 0: no tokens at all
       __syncthreads();
@@ -117,15 +93,11 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
       __syncthreads();
       for (int i = tid; i < kTT * (D / X); i += kThreads) {
         const int t = i % kTT, c = i / kTT;
-        float f[X];
-#pragma unroll
-        for (int e = 0; e < X; ++e) f[e] = 0.f;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
         if (t < n)
-          widen<KV, X>(kb + (int64_t(ids[t / BS]) * p.k_s0 + (c * BS + t % BS) * X) * CS, f);
-#pragma unroll
-        for (int e = 0; e < X; e += 4)
-          *reinterpret_cast<float4 *>(kv + t * kPitch + c * X + e) =
-              make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+          f = __ldg(reinterpret_cast<const float4 *>(kb + int64_t(ids[t / BS]) * p.k_s0 +
+                                                     (c * BS + t % BS) * X));
+        *reinterpret_cast<float4 *>(kv + t * kPitch + c * X) = f;
       }
       __syncthreads();
       float s[4][4];
@@ -157,8 +129,7 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int t = t0 + tg + 16 * j;
-          float x = p.cap > 0.f ? (kExact ? logit.capped_exact(s[i][j]) : logit.capped(s[i][j]))
-                                : logit.plain(s[i][j]);
+          float x = p.cap > 0.f ? logit.capped_exact(s[i][j]) : logit.plain(s[i][j]);
           bool seen = true;
           int kpos = t;
           if (tail && t >= st.q.ctx) {
@@ -194,16 +165,15 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
         l[i] = fmaf(l[i], shrink, sum);
       }
       __syncthreads();
-      for (int i = tid; i < (kTT / VT) * D; i += kThreads) {
-        const int d = i % D, t = i / D * VT;
-        float f[VT];
-#pragma unroll
-        for (int e = 0; e < VT; ++e) f[e] = 0.f;
-        if (t < n) {
-          widen<KV, VT>(vb + (int64_t(ids[t / BS]) * p.v_s0 + d * BS + t % BS) * CS, f);
-        }
-#pragma unroll
-        for (int e = 0; e < VT; ++e) kv[(t + e) * kPitch + d] = t + e < n ? f[e] : 0.f;
+      for (int i = tid; i < (kTT / X) * D; i += kThreads) {
+        const int d = i % D, t = i / D * X;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < n)
+          f = __ldg(reinterpret_cast<const float4 *>(vb + int64_t(ids[t / BS]) * p.v_s0 + d * BS + t % BS));
+        kv[t * kPitch + d] = f.x;  // (t < n: the 4 tokens are of one page; zeros past the end)
+        kv[(t + 1) * kPitch + d] = t + 1 < n ? f.y : 0.f;
+        kv[(t + 2) * kPitch + d] = t + 2 < n ? f.z : 0.f;
+        kv[(t + 3) * kPitch + d] = t + 3 < n ? f.w : 0.f;
       }
       __syncthreads();
       // The tile's products are summed by themselves and then added: next to a
@@ -257,12 +227,12 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
       if (r >= st.rows) continue;
       if (whole) {
         const int R = st.row0 + r;
-        T *o = static_cast<T *>(p.out) + int64_t(st.q.q0 + R / p.group) * p.o_s0 +
+        float *o = static_cast<float *>(p.out) + int64_t(st.q.q0 + R / p.group) * p.o_s0 +
                int64_t(st.kvh * p.group + R % p.group) * p.o_s1;
         const float inv = l[i] == 0.f ? 0.f : __fdiv_rn(p.out_scale, l[i]);
 #pragma unroll
         for (int e = 0; e < D / 16; ++e)
-          o[int64_t((e >> 2) * 64 + tg * 4 + (e & 3)) * p.o_s2] = from_f32<T>(acc[i][e] * inv);
+          o[int64_t((e >> 2) * 64 + tg * 4 + (e & 3)) * p.o_s2] = acc[i][e] * inv;
       } else {
         const int64_t part = (2 * int64_t(blockIdx.x) + (first ? 0 : 1)) * kRT + r;
         if (tg == 0) p.ml[part] = make_float2(m[i], l[i]);
@@ -276,70 +246,35 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
   }
 }
 
-template <typename T, typename KV, int D, int BS>
+template <int D, int BS>
 pkv_status_t launch(const TreeParams &p, int ctas, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
-  auto kernel = tree_simt_kernel<T, KV, D, BS>;
-  constexpr int smem = SimtCfg<T, KV, D>::kSmem;
+  auto kernel = tree_simt_kernel<D, BS>;
+  constexpr int smem = SimtCfg<D>::kSmem;
   if (!detail::ensure_smem_attr(kernel, smem, done)) return PKV_ERR_CUDA;
   return launch_programmatic(kernel, dim3(ctas), dim3(kThreads), smem, stream, p) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }
 
-template <typename T, typename KV, int D>
+template <int D>
 pkv_status_t by_block(const TreeParams &p, int ctas, cudaStream_t s) {
   switch (p.block_size) {
-    case 8: return launch<T, KV, D, 8>(p, ctas, s);
-    case 16: return launch<T, KV, D, 16>(p, ctas, s);
-    case 32: return launch<T, KV, D, 32>(p, ctas, s);
+    case 8: return launch<D, 8>(p, ctas, s);
+    case 16: return launch<D, 16>(p, ctas, s);
+    case 32: return launch<D, 32>(p, ctas, s);
     default: return PKV_ERR_UNSUPPORTED;
   }
-}
-
-template <typename T, typename KV>
-pkv_status_t by_head(const TreeParams &p, int D, int ctas, cudaStream_t s) {
-  switch (D) {
-    case 64: return by_block<T, KV, 64>(p, ctas, s);
-    case 128: return by_block<T, KV, 128>(p, ctas, s);
-    case 256:
-      if constexpr (!std::is_same<T, float>::value) return by_block<T, KV, 256>(p, ctas, s);
-      return PKV_ERR_UNSUPPORTED;
-    default: return PKV_ERR_UNSUPPORTED;
-  }
-}
-
-template <typename T>
-pkv_status_t by_cache(const TreeParams &p, int32_t kv, int D, int ctas, cudaStream_t s) {
-  if (kv == PKV_KV_AUTO) return by_head<T, T>(p, D, ctas, s);
-  if constexpr (!std::is_same<T, float>::value) {
-    if (kv == PKV_KV_FP8_E4M3) return by_head<T, fp8_e4m3_t>(p, D, ctas, s);
-    return by_head<T, fp8_e5m2_t>(p, D, ctas, s);
-  }
-  return PKV_ERR_UNSUPPORTED;
 }
 
 }  // namespace
 
-pkv_status_t launch_tree_simt(const pkv_decode_args_t *a, TreeParams &p, void *workspace,
-                              cudaStream_t stream) {
-  const int D = a->head_size;
-  const int ctas = tree_sm_count() * kTreeSimtCtasPerSm;
-  uint8_t *w = static_cast<uint8_t *>(workspace);
-  p.cuts = reinterpret_cast<TreeCut *>(w);
-  w += (size_t(ctas) * sizeof(TreeCut) + 255) / 256 * 256;
-  p.ml = reinterpret_cast<float2 *>(w);
-  w += size_t(2) * ctas * kRT * sizeof(float2);
-  p.acc = reinterpret_cast<float *>(w);
-  pkv_status_t st;
-  switch (a->dtype) {
-    case PKV_F32: st = by_cache<float>(p, a->kv_cache_dtype, D, ctas, stream); break;
-    case PKV_F16: st = by_cache<__half>(p, a->kv_cache_dtype, D, ctas, stream); break;
-    case PKV_BF16: st = by_cache<__nv_bfloat16>(p, a->kv_cache_dtype, D, ctas, stream); break;
+pkv_status_t launch_tree_simt(const TreeParams &p, int D, int ctas, cudaStream_t stream) {
+  switch (D) {
+    case 64: return by_block<64>(p, ctas, stream);
+    case 128: return by_block<128>(p, ctas, stream);
     default: return PKV_ERR_UNSUPPORTED;
   }
-  if (st != PKV_OK) return st;
-  return launch_tree_join(p, a->dtype, D, kRT, ctas, stream);
 }
 
 }  // namespace pkv
