@@ -71,6 +71,7 @@ struct TreeTcCfg {
   // Mask buffers: a value slot is refilled only after the product of the tile
   // (OS + 1) / 2 before, and with it that tile's softmax, is done.
   static constexpr int MB = (OS + 1) / 2;
+  static_assert(MB <= 4, "k_ready and v_ready are reused every 4 tiles");
   static constexpr int kWords = TT / 32;        // mask words of a tile
   static constexpr int kSoftWarps = 4 * NWG;
   static constexpr int kThreads = (kSoftWarps + 6) * 32;
@@ -185,7 +186,10 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff);
   uint64_t *raw_full = bars + 0;     // [RS <= 8] pages landed (tx bytes)
   uint64_t *raw_free = bars + 8;     // [RS] 8-bit caches: widened (4 prep warps)
-  uint64_t *op_ready = bars + 16;    // [OS <= 8] operand ready (4 prep warps)
+  // Operands ready, by tile modulo 4 and not by slot (16-bit keys need no prep,
+  // and with an odd number of slots a slot holds keys and values in turn).
+  uint64_t *k_ready = bars + 16;     // [4] 8-bit caches: keys widened (4 prep warps)
+  uint64_t *v_ready = bars + 20;     // [4] values in operand layout (4 prep warps)
   uint64_t *op_free = bars + 24;     // [OS] MMAs on the slot done (commit)
   uint64_t *s_full = bars + 32;      // [2] scores in TMEM (commit)
   uint64_t *p_full = bars + 34;      // [2] probabilities written (4 warps)
@@ -213,9 +217,10 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_free[i], 4);
     }
-    for (int i = 0; i < OS; ++i) {
-      mbar_init(&op_ready[i], 4);
-      mbar_init(&op_free[i], 1);
+    for (int i = 0; i < OS; ++i) mbar_init(&op_free[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&k_ready[i], 4);
+      mbar_init(&v_ready[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -564,7 +569,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tc::mbar_arrive(&op_ready[os]);
+            tc::mbar_arrive(kv == 0 ? &k_ready[g & 3] : &v_ready[g & 3]);
             if (kFp8) tc::mbar_arrive(&raw_free[rs]);
           }
         }
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
       const int64_t n = 2 * pend + 1;
       const int os = int(n % OS);
       if (!wait_one(&p_full[b], uint32_t(pend >> 1) & 1u) ||
-          !wait_one(&op_ready[os], uint32_t(n / OS) & 1u) ||
+          !wait_one(&v_ready[pend & 3], uint32_t(pend >> 2) & 1u) ||
           (pend_fresh && pend_unit > 0 && !wait_one(o_free, uint32_t(pend_unit - 1) & 1u)))
         return false;
       if (!kFp8 && !wait_one(&raw_full[os], uint32_t(n / OS) & 1u)) return false;
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
           const int b = int(g & 1);
           const int64_t n = 2 * g;
           const int os = int(n % OS);
-          ok = kFp8 ? wait_one(&op_ready[os], uint32_t(n / OS) & 1u)
+          ok = kFp8 ? wait_one(&k_ready[g & 3], uint32_t(g >> 2) & 1u)
                     : wait_one(&raw_full[os], uint32_t(n / OS) & 1u);
           // the score buffer holds the probabilities of tile g - 2 until its product is done
           if (ok && g >= 2) ok = wait_one(&pv_done[b], uint32_t((g >> 1) - 1) & 1u);
@@ -707,8 +712,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
         bool any_hurt = false;
         if (tail) {
           // the prep warps' mask words and marks come with the value tile
-          const int64_t n = 2 * g + 1;
-          if (!wait_warp(&op_ready[n % OS], uint32_t(n / OS) & 1u)) {
+          if (!wait_warp(&v_ready[g & 3], uint32_t(g >> 2) & 1u)) {
             failed = true;
             break;
           }

@@ -160,6 +160,15 @@ def test_long_sequence_split_over_the_gpu(dtype, kv):
     assert_attention_close(_run(inp), _oracle(inp), DT[dtype], "split")
 
 
+@pytest.mark.parametrize("dtype,kv,D,bs", [
+    ("bf16", "auto", 128, 16), ("bf16", "auto", 128, 32), ("f16", "auto", 64, 8), ("bf16", "auto", 256, 32),
+    ("bf16", "fp8_e4m3", 128, 16), ("f16", "fp8_e5m2", 64, 32), ("bf16", "fp8_e5m2", 256, 8), ("f32", "auto", 64, 16)])
+def test_many_tiles_to_a_cta(dtype, kv, D, bs):
+    """Every CTA goes many times round its ring of tiles, across units."""
+    inp = _batch(dtype, kv, D, bs, 8, 8, [6011, 37, 4999, 7001], [2, 5, 3, 1], 19, peaky_fraction=0.01)
+    assert_attention_close(_run(inp), _oracle(inp), DT[dtype], "tiles")
+
+
 @pytest.mark.parametrize("dtype,kv", [("bf16", "auto"), ("f32", "auto"), ("f16", "fp8_e5m2")])
 def test_many_short_sequences(dtype, kv):
     """More units than CTAs, several sequences to a CTA; empty ones between."""
