@@ -640,7 +640,7 @@ pkv_status_t paged_attention_tree(void *out, const int64_t out_stride[3],
   uint8_t *base = static_cast<uint8_t *>(tree->workspace);
   p.cuts = reinterpret_cast<pkv::TreeCut *>(base);
   p.ml = reinterpret_cast<float2 *>(base + w.ml);
-  p.acc = reinterpret_cast<float *>(base + w.acc);
+  p.acc = reinterpret_cast<float4 *>(base + w.acc);
   const int D = args->head_size;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool e4m3 = args->kv_cache_dtype == PKV_KV_FP8_E4M3;
@@ -655,7 +655,7 @@ pkv_status_t paged_attention_tree(void *out, const int64_t out_stride[3],
               : (e4m3 ? pkv::launch_tree_tc_bf16_e4m3(p, D, w.ctas, s)
                       : pkv::launch_tree_tc_bf16_e5m2(p, D, w.ctas, s));
   if (st != PKV_OK) return st;
-  return pkv::launch_tree_join(p, args->dtype, D, w.rows, w.ctas, s);
+  return pkv::launch_tree_join(p, args->dtype, D, w.ctas, s);
 }
 
 }  // extern "C"

@@ -27,9 +27,10 @@ namespace pkv {
 // describes it for the join.
 struct TreeCut {
   int32_t valid;
-  int32_t q0, rows, kvh, row0;  // first query row, rows of the (sequence, kv head), row tile
-  int32_t parts;                // CTAs of the split grid
-  int64_t begin, end, total;    // the unit's tiles among all `total`
+  int32_t q0, rows, kvh, row0;  // first query row of the sequence, rows of the tile from row0 on
+  int32_t parts;                // CTAs of the split
+  int64_t begin, end;           // the unit's tiles among all
+  int64_t each, extra;          // tiles of a run; the first `extra` runs have one more
 };
 
 struct TreeParams {
@@ -52,8 +53,10 @@ struct TreeParams {
   void *out;
   int64_t o_s0, o_s1, o_s2;
   TreeCut *cuts;  // workspace: [CTAs]
-  float2 *ml;     // workspace: [2 * CTAs][RT] (m, l)
-  float *acc;     // workspace: [2 * CTAs][RT][D]
+  // Partial results, two per CTA: (m, l) of each row, and the sums, four dims of
+  // a row together and rows adjacent (threads are rows).
+  float2 *ml;   // workspace: [2 * CTAs][RT]
+  float4 *acc;  // workspace: [2 * CTAs][D / 4][RT]
   int32_t num_seqs, num_tokens, num_heads, num_kv_heads, group, num_blocks, max_blocks_per_seq;
   int32_t block_size, mask_cols;
   float scale;      // of the score: args->scale (x k_scale for fp8 caches)
@@ -131,72 +134,94 @@ __device__ __forceinline__ int tree_block_id(const TreeParams &p, int64_t row, i
   return id;
 }
 
-// Where CTA `c` of `parts` starts among `total` tiles.
-__host__ __device__ __forceinline__ int64_t tree_start(int64_t total, int c, int parts) {
-  return total / parts * c + total % parts * c / parts;
+// a / b for a >= 0, b > 0: 32-bit wherever they fit (a 64-bit division is a few
+// hundred cycles on the way to a CTA's first load).
+__device__ __forceinline__ int64_t tree_div(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return int64_t(uint32_t(a) / uint32_t(b));
+  return a / b;
 }
 
-// A CTA's place in the work: its run [begin, end) of tiles and the sequence
+// A CTA's place in the work: its run [begin, end) of tiles, and the sequence
 // that `begin` falls into (`base`: that sequence's first tile).
 struct TreeRun {
-  int64_t total, begin, end, base;
+  int64_t begin, end, base, each, extra;
   int32_t seq, parts;
+  TreeSeq q;
+  // Where the run of CTA c starts.
+  __device__ __forceinline__ int64_t start_of(int64_t c) const {
+    return each * c + (c < extra ? c : extra);
+  }
+};
+
+// Shared memory of tree_find_run.
+template <int NT>
+struct TreeScratch {
+  int64_t sums[NT / 32];
+  int64_t base;
+  int32_t seq;
+  TreeSeq q;
 };
 
 // Sums the batch's tiles over the CTA's NT threads and finds the run of CTA
 // blockIdx.x.  Every thread returns the same run; begin == end: nothing to do.
-// `scratch`: NT / 32 + 3 words of shared memory, free again after the call's
-// last barrier has been passed by a later __syncthreads().
 template <int TT, int RT, int NT>
-__device__ __forceinline__ TreeRun tree_find_run(const TreeParams &p, int64_t *scratch) {
+__device__ __forceinline__ TreeRun tree_find_run(const TreeParams &p, TreeScratch<NT> &sh) {
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.num_seqs + NT - 1) / NT;
-  const int s0 = min(int64_t(tid) * per, int64_t(p.num_seqs));
+  // a thread's sequences: one, or a piece of a longer batch
+  const int per = p.num_seqs <= NT ? 1 : (p.num_seqs + NT - 1) / NT;
+  const int s0 = int(min(int64_t(tid) * per, int64_t(p.num_seqs)));
   const int s1 = min(s0 + per, p.num_seqs);
   int64_t mine = 0;
-  for (int s = s0; s < s1; ++s)
-    mine += tree_weight(p, tree_seq<TT, RT>(p, s, blockIdx.x == 0));
+  TreeSeq q = {};
+  for (int s = s0; s < s1; ++s) {
+    q = tree_seq<TT, RT>(p, s, blockIdx.x == 0);
+    mine += tree_weight(p, q);
+  }
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
-  if (lane == 31) scratch[warp] = incl;
+  if (lane == 31) sh.sums[warp] = incl;
   __syncthreads();
   int64_t before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const int64_t t = scratch[w];
+    const int64_t t = sh.sums[w];
     if (w < warp) before += t;
     total += t;
   }
   TreeRun r;
-  r.total = total;
   r.parts = int(min(int64_t(gridDim.x), total));
-  r.begin = r.end = 0;
-  r.base = 0;
+  r.begin = r.end = r.base = r.each = r.extra = 0;
   r.seq = 0;
   if (int(blockIdx.x) >= r.parts) return r;  // the same for every thread
-  r.begin = tree_start(total, blockIdx.x, r.parts);
-  r.end = tree_start(total, blockIdx.x + 1, r.parts);
+  r.each = tree_div(total, r.parts);
+  r.extra = total - r.each * r.parts;
+  r.begin = r.start_of(blockIdx.x);
+  r.end = r.start_of(int64_t(blockIdx.x) + 1);
   const int64_t first = before + incl - mine;
   if (r.begin >= first && r.begin < first + mine) {
     int64_t at = first;
-    for (int s = s0; s < s1; ++s) {
-      const int64_t w = tree_weight(p, tree_seq<TT, RT>(p, s, false));
-      if (r.begin < at + w) {
-        scratch[NW] = s;
-        scratch[NW + 1] = at;
-        break;
+    int s = s0;
+    if (per > 1) {
+      for (; s < s1; ++s) {
+        q = tree_seq<TT, RT>(p, s, false);
+        const int64_t w = tree_weight(p, q);
+        if (r.begin < at + w) break;
+        at += w;
       }
-      at += w;
     }
+    sh.seq = s;
+    sh.base = at;
+    sh.q = q;
   }
   __syncthreads();
-  r.seq = int(scratch[NW]);
-  r.base = scratch[NW + 1];
+  r.seq = sh.seq;
+  r.base = sh.base;
+  r.q = sh.q;
   return r;
 }
 
@@ -221,7 +246,7 @@ struct TreeWalk {
     pos = r.begin;
     base = r.base;
     seq = r.seq;
-    q = tree_seq<TT, RT>(p, seq, false);
+    q = r.q;
   }
   __device__ __forceinline__ bool next(const TreeParams &p, TreeStretch &s) {
     if (pos >= run.end) return false;
@@ -232,10 +257,10 @@ struct TreeWalk {
       q = tree_seq<TT, RT>(p, seq, false);
     }
     const int64_t off = pos - base;
-    const int64_t u = off / q.tiles;
+    const int64_t u = tree_div(off, q.tiles);
     s.seq = seq;
     s.q = q;
-    s.kvh = int(u / q.row_tiles);
+    s.kvh = q.row_tiles == 1 ? int(u) : int(tree_div(u, q.row_tiles));
     s.row0 = int(u - int64_t(s.kvh) * q.row_tiles) * RT;
     s.rows = int(min(int64_t(RT), int64_t(q.T) * p.group - s.row0));
     s.tile0 = int(off - u * q.tiles);
@@ -255,13 +280,14 @@ __device__ __forceinline__ void tree_write_cut(const TreeParams &p, const TreeRu
     c.begin = r.begin - s->tile0;
     c.end = c.begin + s->tiles;
     // the first run that starts inside the unit describes it
-    c.valid = tree_start(r.total, int(blockIdx.x) - 1, r.parts) <= c.begin;
+    c.valid = r.start_of(int64_t(blockIdx.x) - 1) <= c.begin;
     c.q0 = s->q.q0;
     c.rows = s->rows;
     c.kvh = s->kvh;
     c.row0 = s->row0;
     c.parts = r.parts;
-    c.total = r.total;
+    c.each = r.each;
+    c.extra = r.extra;
   }
   p.cuts[blockIdx.x] = c;
 }
@@ -301,8 +327,8 @@ pkv_status_t launch_tree_tc_f16_e4m3(const TreeParams &p, int head_size, int cta
 pkv_status_t launch_tree_tc_f16_e5m2(const TreeParams &p, int head_size, int ctas, cudaStream_t s);
 pkv_status_t launch_tree_tc_bf16_e4m3(const TreeParams &p, int head_size, int ctas, cudaStream_t s);
 pkv_status_t launch_tree_tc_bf16_e5m2(const TreeParams &p, int head_size, int ctas, cudaStream_t s);
-// `rows`: the kernel's row tile, `ctas`: its grid.
-pkv_status_t launch_tree_join(const TreeParams &p, pkv_dtype_t dtype, int head_size, int rows,
-                              int ctas, cudaStream_t stream);
+// `ctas`: the attention kernel's grid.
+pkv_status_t launch_tree_join(const TreeParams &p, pkv_dtype_t dtype, int head_size, int ctas,
+                              cudaStream_t stream);
 
 }  // namespace pkv

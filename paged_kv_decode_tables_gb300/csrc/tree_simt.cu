@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
   float *qs = tree_simt_smem;
   float *kv = qs + kRT * kPitch;
   float *ps = kv + kTT * kPitch;
-  __shared__ int64_t scratch[kThreads / 32 + 3];
+  __shared__ TreeScratch<kThreads> scratch;
   __shared__ int ids[kTT / 8];
   const int tid = threadIdx.x, rg = tid >> 4, tg = tid & 15;
   grid_dependency_wait();
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
         if (tg == 0) p.ml[part] = make_float2(m[i], l[i]);
 #pragma unroll
         for (int e = 0; e < D / 64; ++e)
-          *reinterpret_cast<float4 *>(p.acc + part * D + e * 64 + tg * 4) =
+          p.acc[((part - r) / kRT * (D / 4) + e * 16 + tg) * kRT + r] =
               make_float4(acc[i][4 * e], acc[i][4 * e + 1], acc[i][4 * e + 2], acc[i][4 * e + 3]);
       }
     }

@@ -128,7 +128,7 @@ struct TreeTcCfg {
   static constexpr int kUnitOff = kQScaleOff + (kFp8 ? kUnits * kTreeTcRows * 4 : 0);  // [kUnits]
   static constexpr int kBarOff = kUnitOff + kUnits * 64;
   static constexpr int kScratchOff = kBarOff + 100 * 8;
-  static constexpr int kSmem = kScratchOff + (kThreads / 32 + 3) * 8 + 16;
+  static constexpr int kSmem = kScratchOff + int(sizeof(TreeScratch<kThreads>));
   static_assert(kSmem <= 232448, "shared memory");
   // Column (within a score buffer) of the tile's token t, and the token of a column.
   static __host__ __device__ constexpr int column(int t) {
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
   uint32_t *bad = reinterpret_cast<uint32_t *>(smem + Cfg::kBadOff);     // [MB][4]
   float2 *stats = reinterpret_cast<float2 *>(smem + Cfg::kStatOff);      // [2][2][128]
   float *qscale = reinterpret_cast<float *>(smem + Cfg::kQScaleOff);     // [kUnits][128]
-  int64_t *scratch = reinterpret_cast<int64_t *>(smem + Cfg::kScratchOff);
+  auto &scratch = *reinterpret_cast<TreeScratch<Cfg::kThreads> *>(smem + Cfg::kScratchOff);
   auto unit_at = [&](int u) {
     return reinterpret_cast<TreeTcUnit *>(smem + Cfg::kUnitOff + (u % Cfg::kUnits) * 64);
   };
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
             } else {
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4 *>(p.acc + part * D + c + e) =
+                p.acc[((part - r) / RT * (D / 4) + (c + e) / 4) * RT + r] =
                     make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
             }
           }
