@@ -310,7 +310,9 @@ struct TreeLogit {
   }
   __device__ __forceinline__ float capped(float d) const {
     const float e = ex2(d * (cap_arg * 2.88539008177792681472f));
-    return fmaf(-2.f * cap_log2, __frcp_rn(1.f + e), cap_log2);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return fmaf(-2.f * cap_log2, r, cap_log2);
   }
 };
 

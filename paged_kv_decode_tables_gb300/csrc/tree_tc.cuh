@@ -110,6 +110,9 @@ struct TreeTcCfg {
   static constexpr int kSoftRegs = 168, kPrepRegs = 104, kIssueRegs = 72;
   static_assert(NWG == 1 || (2 * kSoftRegs + kPrepRegs + kIssueRegs) * 128 == kThreads * 128, "registers");
   static constexpr int kUnits = 4;              // unit descriptors in flight
+  // Query scales (8-bit caches): written up to two units ahead of the score MMAs,
+  // read up to NSB units behind them.
+  static constexpr int kQScales = 8;
 
   // Tensor memory: output accumulators, queries, score buffers.
   static constexpr uint32_t kTmemCols = 512;
@@ -124,8 +127,8 @@ struct TreeTcCfg {
   static constexpr int kMaskOff = kRawOff + (kFp8 ? RS * kRawTile : 0);
   static constexpr int kBadOff = kMaskOff + MB * kTreeTcRows * kWords * 4;
   static constexpr int kStatOff = kBadOff + MB * 16;                    // [2][2][128] (m, l)
-  static constexpr int kQScaleOff = kStatOff + 4 * kTreeTcRows * 8;     // [kUnits][128]
-  static constexpr int kUnitOff = kQScaleOff + (kFp8 ? kUnits * kTreeTcRows * 4 : 0);  // [kUnits]
+  static constexpr int kQScaleOff = kStatOff + 4 * kTreeTcRows * 8;     // [kQScales][128]
+  static constexpr int kUnitOff = kQScaleOff + (kFp8 ? kQScales * kTreeTcRows * 4 : 0);  // [kUnits]
   static constexpr int kBarOff = kUnitOff + kUnits * 64;
   static constexpr int kScratchOff = kBarOff + 100 * 8;
   static constexpr int kSmem = kScratchOff + int(sizeof(TreeScratch<kThreads>));
@@ -212,7 +215,25 @@ __device__ __forceinline__ void ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
 
 }  // namespace tc
 
-template <typename T, typename KV, int D, int BS>
+// Bounded wait that gives up with the CTA's other roles (see tc_wait), in few
+// instructions: it stands in two dozen places of a kernel whose loops just
+// about fit the instruction cache.
+__device__ __forceinline__ bool tree_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                          volatile int *abort) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit_ns) *abort = 1;
+    if (*abort) return false;
+  }
+  return true;
+}
+
+// BIASED: scores are capped or biased (or their scale is not positive).  A kernel
+// of its own: the loops of all roles just about fit the instruction cache, and
+// code that a call does not need costs it speed.
+template <typename T, typename KV, int D, int BS, bool BIASED>
 __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
     tree_tc_kernel(const TreeParams p) {
   using Cfg = TreeTcCfg<T, KV, D, BS>;
@@ -255,7 +276,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
   uint32_t *masks = reinterpret_cast<uint32_t *>(smem + Cfg::kMaskOff);  // [MB][128][kWords]
   uint32_t *bad = reinterpret_cast<uint32_t *>(smem + Cfg::kBadOff);     // [MB][4]
   float2 *stats = reinterpret_cast<float2 *>(smem + Cfg::kStatOff);      // [2][2][128]
-  float *qscale = reinterpret_cast<float *>(smem + Cfg::kQScaleOff);     // [kUnits][128]
+  float *qscale = reinterpret_cast<float *>(smem + Cfg::kQScaleOff);     // [kQScales][128]
   auto &scratch = *reinterpret_cast<TreeScratch<Cfg::kThreads> *>(smem + Cfg::kScratchOff);
   auto unit_at = [&](int u) {
     return reinterpret_cast<TreeTcUnit *>(smem + Cfg::kUnitOff + (u % Cfg::kUnits) * 64);
@@ -302,9 +323,9 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
   const uint64_t drain_ns = min(wait_ns, uint64_t(100000000ull));
   bool failed = false;
 
-  auto wait_one = [&](uint64_t *bar, uint32_t parity) { return tc_wait(bar, parity, wait_ns, abort_flag); };
+  auto wait_one = [&](uint64_t *bar, uint32_t parity) { return tree_wait(bar, parity, wait_ns, abort_flag); };
   auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
-    return bool(__all_sync(FULL, tc_wait(bar, parity, wait_ns, abort_flag)));
+    return bool(__all_sync(FULL, tree_wait(bar, parity, wait_ns, abort_flag)));
   };
   // A consumer warp's copy of unit u's descriptor.
   auto take_unit = [&](int u, TreeTcUnit &d) {
@@ -338,11 +359,10 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
       const int node_at = node - d.row0 / p.group;
       float rowscale = 1.f, slope = 0.f;
       int qpos = 0;
-      if (p.alibi) {
+      if (BIASED && p.alibi) {
         slope = p.alibi[head] * kLog2e;
         qpos = p.positions ? p.positions[d.q0 + node] : d.ctx + node;
       }
-      const bool simple = p.cap == 0.f && !p.alibi && p.scale > 0.f;
       float m = -INFINITY, l = 0.f;  // m: the reference that the accumulator is scaled to
       bool have = false;             // this group's accumulator holds something
       uint32_t mine = 0;             // its last tile
@@ -374,36 +394,62 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
           }
         }
         if (live) {
-          if (kFp8) rowscale = qscale[(u % Cfg::kUnits) * RT + min(r, d.rows - 1)];
+          if (kFp8) rowscale = qscale[(u % Cfg::kQScales) * RT + min(r, d.rows - 1)];
           float mul = logit.scale_log2 * rowscale, top = -INFINITY;
-          if (!simple || tail) {
-            // Not only to be scaled: the scores are replaced by their final values
-            // in log2 units first.  (A small loop: it runs once or twice a unit,
-            // mostly from a cold instruction cache.)
+          if (tail) {
+            // Masked: the scores are replaced by their final values in log2 units
+            // first.  (A small loop: it runs once or twice a unit, mostly from a
+            // cold instruction cache.)
 #pragma unroll 1
-            for (int k = 0; k < TT / 16; ++k) {
-              float z[16];
-              tc::ld_x16(s + uint32_t(16 * k), z);
+            for (int k = 0; k < TT / 8; ++k) {
+              uint32_t z[8];
+              tc::ld_x8(s + uint32_t(8 * k), z);
               tc::wait_ld();
+              const int t8 = Cfg::token(8 * k);  // 8 tokens from here on
+              const uint32_t bits = masks[(mb * RT + node_at) * kWords + (t8 >> 5)] >> (t8 & 31);
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int t8 = Cfg::token(16 * k + 8 * q);  // 8 tokens from here on
-                const uint32_t bits =
-                    tail ? masks[(mb * RT + node_at) * kWords + (t8 >> 5)] >> (t8 & 31) : FULL;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float y = z[8 * q + e] * rowscale;
-                  float x = p.cap > 0.f ? logit.capped(y) : logit.plain(y);
-                  if (p.alibi) {
-                    const int t = t0 + t8 + e;
-                    int kpos = t;
-                    if (p.positions && t >= d.ctx && t < d.L) kpos = p.positions[d.q0 + t - d.ctx];
-                    x = fmaf(slope, float(kpos - qpos), x);
-                  }
-                  z[8 * q + e] = (bits >> e) & 1u ? x : -INFINITY;
+              for (int e = 0; e < 8; ++e) {
+                const float y = __uint_as_float(z[e]) * rowscale;
+                float x = BIASED && p.cap > 0.f ? logit.capped(y) : logit.plain(y);
+                if (BIASED && p.alibi) {
+                  const int t = t0 + t8 + e;
+                  int kpos = t;
+                  if (p.positions && t >= d.ctx && t < d.L) kpos = p.positions[d.q0 + t - d.ctx];
+                  x = fmaf(slope, float(kpos - qpos), x);
                 }
+                z[e] = __float_as_uint((bits >> e) & 1u ? x : -INFINITY);
               }
-              tc::st_x16(s + uint32_t(16 * k), z);
+              tc::st_x8(s + uint32_t(8 * k), z);
+            }
+            tc::wait_st();
+            mul = 1.f;
+          } else if constexpr (BIASED) {
+            // Every row sees the tile, but its scores are capped or biased: the
+            // same, half a tile at a time.  (Through tensor memory as well: beside
+            // the 64 registers of the common path below there is no room for it.)
+            const float b0 = slope * float(t0 - qpos);
+#pragma unroll 1
+            for (int h = 0; h < TT; h += 32) {
+              uint32_t z[32];
+              tc::ld_x32(s + uint32_t(h), z);
+              tc::wait_ld();
+              if (p.cap > 0.f) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  z[e] = __float_as_uint(logit.capped(__uint_as_float(z[e]) * rowscale));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) z[e] = __float_as_uint(__uint_as_float(z[e]) * mul);
+              }
+              if (p.alibi) {
+                // the bias of column h + e's token is slope * (t0 - qpos + token)
+                const float bh = fmaf(slope, float(Cfg::token(h)), b0);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  z[e] = __float_as_uint(__uint_as_float(z[e]) + fmaf(slope, float(Cfg::token(e)), bh));
+              }
+              tc::st_x16u(s + uint32_t(h), reinterpret_cast<const uint32_t(&)[16]>(z[0]));
+              tc::st_x16u(s + uint32_t(h + 16), reinterpret_cast<const uint32_t(&)[16]>(z[16]));
             }
             tc::wait_st();
             mul = 1.f;
@@ -667,9 +713,9 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
           int k = 0;
           if (amax > 0.f && amax < INFINITY) k = clamp_int(141 - int(__float_as_uint(amax) >> 23), -100, 100);
           up = __uint_as_float(uint32_t(127 + k) << 23);
-          qscale[(u % Cfg::kUnits) * RT + pt] = __uint_as_float(uint32_t(127 - k) << 23);
+          qscale[(u % Cfg::kQScales) * RT + pt] = __uint_as_float(uint32_t(127 - k) << 23);
         } else {
-          if (kFp8) qscale[(u % Cfg::kUnits) * RT + pt] = 1.f;
+          if (kFp8) qscale[(u % Cfg::kQScales) * RT + pt] = 1.f;
           fetch(0);
         }
       }

@@ -10,16 +10,23 @@
 namespace pkv {
 namespace detail {
 
-template <typename T, typename KV, int D, int BS>
-pkv_status_t launch_tree_tc_as(const TreeParams &p, int ctas, cudaStream_t stream) {
+template <typename T, typename KV, int D, int BS, bool BIASED>
+pkv_status_t launch_tree_tc_kernel(const TreeParams &p, int ctas, cudaStream_t stream) {
   using Cfg = TreeTcCfg<T, KV, D, BS>;
   static std::atomic<unsigned long long> done{0};
-  auto kernel = tree_tc_kernel<T, KV, D, BS>;
+  auto kernel = tree_tc_kernel<T, KV, D, BS, BIASED>;
   if (!ensure_smem_attr(kernel, Cfg::kSmem, done)) return PKV_ERR_CUDA;
   return launch_programmatic(kernel, dim3(ctas), dim3(Cfg::kThreads), Cfg::kSmem, stream, p) ==
                  cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
+}
+
+template <typename T, typename KV, int D, int BS>
+pkv_status_t launch_tree_tc_as(const TreeParams &p, int ctas, cudaStream_t stream) {
+  if (p.cap > 0.f || p.alibi != nullptr || !(p.scale > 0.f))
+    return launch_tree_tc_kernel<T, KV, D, BS, true>(p, ctas, stream);
+  return launch_tree_tc_kernel<T, KV, D, BS, false>(p, ctas, stream);
 }
 
 template <typename T, typename KV, int D>
