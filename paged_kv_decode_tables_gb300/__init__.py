@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -230,19 +231,18 @@ def lib() -> ctypes.CDLL:
                                              ctypes.POINTER(DecodeArgs), _c_p]
     L.pkv_noalloc_scratch_bytes.restype = ctypes.c_size_t
     L.pkv_noalloc_scratch_bytes.argtypes = []
-    for name, struct in (("cache_write", CacheWriteArgs), ("cache_read", CacheReadArgs),
-                         ("tree", TreeArgs)):
+    for name, args in (("cache_write", CacheWriteArgs), ("cache_read", CacheReadArgs),
+                       ("tree", TreeArgs)):
         size = getattr(L, f"pkv_{name}_args_size")
         size.restype, size.argtypes = ctypes.c_size_t, []
-        if size() != ctypes.sizeof(struct):
+        if size() != ctypes.sizeof(args):
             raise RuntimeError(f"pkv_{name}_args_t layout mismatch")
     L.paged_kv_write.restype = ctypes.c_int
-    L.paged_kv_write.argtypes = [ctypes.POINTER(CacheWriteArgs), _c_p]
+    L.paged_kv_write.argtypes = [_c_p, _c_p]
     L.paged_kv_read.restype = ctypes.c_int
-    L.paged_kv_read.argtypes = [ctypes.POINTER(CacheReadArgs), _c_p]
+    L.paged_kv_read.argtypes = [_c_p, _c_p]
     L.paged_attention_tree.restype = ctypes.c_int
-    L.paged_attention_tree.argtypes = [_c_p, ctypes.POINTER(_c_i64), ctypes.POINTER(DecodeArgs),
-                                       ctypes.POINTER(TreeArgs), _c_p]
+    L.paged_attention_tree.argtypes = [_c_p, ctypes.POINTER(_c_i64), _c_p, _c_p, _c_p]
     L.pkv_tree_workspace_bytes.restype = ctypes.c_size_t
     L.pkv_tree_workspace_bytes.argtypes = [_c_i32]
     if L.pkv_decode_args_size() != ctypes.sizeof(DecodeArgs):
@@ -705,33 +705,52 @@ def paged_attention_v2_noalloc(out: torch.Tensor, query: torch.Tensor, key_cache
            "paged_attention_v2_noalloc")
 
 
-def _same_device(first: torch.Tensor, *named) -> torch.device:
-    """The one CUDA device of all tensors (None entries are skipped)."""
-    dev = first.device
+def _one_device(dev: int, named) -> None:
+    """All tensors (None entries are skipped) on CUDA device ``dev``."""
     for t, n in named:
-        _cuda(t, n)
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, not on {dev}")
-    return dev
+        if t is not None and t.get_device() != dev:
+            _cuda(t, n)
+            raise ValueError(f"{n} is on {t.device}, not on cuda:{dev}")
 
 
-def _call_on(dev: torch.device, stream, what: str, call) -> None:
-    """``call(stream)`` with ``dev`` current, on ``stream`` or that device's current stream."""
-    if dev.index == torch.cuda.current_device():
-        _check(call(_stream(stream)), what)
+def _cuda_index(t: torch.Tensor, name: str) -> int:
+    _cuda(t, name)
+    return t.get_device()
+
+
+# The raw handle of a device's current stream, without a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call_on(dev: int, stream, what: str, fn, *args) -> None:
+    """``fn(*args, stream)`` with ``dev`` current, on ``stream`` or that device's current stream."""
+    if stream is None and _raw_stream is not None:
+        raw = _raw_stream(dev)
+    elif stream is None:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        raw = _stream(stream)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            _check(call(_stream(stream)), what)
+            status = fn(*args, raw)
+    if status != PKV_OK:
+        _check(status, what)
 
 
-def _fill_strides(array, t: torch.Tensor) -> None:
-    for i, s in enumerate(t.stride()):
-        array[i] = s
+# The argument structs packed in one go (a ctypes structure filled field by
+# field costs a small call more time on the host than on the GPU).
+_PACK_WRITE = struct.Struct("@8i2fP3qP3qP5qP4qPqP")
+_PACK_READ = struct.Struct("@10i2fP3qP3qP5qP4qP2qPPPP")
+_PACK_DECODE = struct.Struct("@9ifP3qP5qP4qP2qPPPi2fPP")
+_PACK_TREE = struct.Struct("@2iPP2qPfPN")
+assert (_PACK_WRITE.size, _PACK_READ.size, _PACK_DECODE.size, _PACK_TREE.size) == tuple(
+    ctypes.sizeof(c) for c in (CacheWriteArgs, CacheReadArgs, DecodeArgs, TreeArgs))
 
 
-def _cache_io_args(a, key, value, names, key_cache, value_cache, kv_cache_dtype, k_scale,
-                   v_scale) -> None:
-    """Fields that ``CacheWriteArgs`` and ``CacheReadArgs`` share."""
+def _check_cache_io(key, value, names, key_cache, value_cache):
+    """Checks that the cache read and write share; the caches' shape."""
     if key.dtype not in _DTYPE_CODE:
         raise ValueError(f"unsupported dtype {key.dtype}")
     if value.dtype != key.dtype:
@@ -739,21 +758,13 @@ def _cache_io_args(a, key, value, names, key_cache, value_cache, kv_cache_dtype,
     if key.dim() != 3 or key_cache.dim() != 5 or value_cache.dim() != 4:
         raise ValueError(f"expected {names[0]} and {names[1]} [N,Hk,D], key_cache [NB,Hk,D/x,bs,x], "
                          "value_cache [NB,Hk,D,bs]")
-    nb, hk, dx, bs, x = key_cache.shape
-    if tuple(value_cache.shape) != (nb, hk, dx * x, bs):
+    nb, hk, dx, bs, x = shape = key_cache.shape
+    if value_cache.shape != (nb, hk, dx * x, bs):
         raise ValueError("key_cache and value_cache do not belong together")
-    if key.shape != value.shape or tuple(key.shape[1:]) != (hk, dx * x):
+    rows = key.shape
+    if rows != value.shape or rows[1] != hk or rows[2] != dx * x:
         raise ValueError(f"{names[0]} and {names[1]} must be [N, {hk}, {dx * x}] for these caches")
-    a.num_tokens, a.num_kv_heads, a.head_size = key.shape
-    a.block_size, a.x, a.num_blocks = bs, x, nb
-    a.dtype = _DTYPE_CODE[key.dtype]
-    a.kv_cache_dtype = _kv_cache_code(key_cache, value_cache, key, kv_cache_dtype)
-    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
-    _fill_strides(a.key_stride, key)
-    _fill_strides(a.value_stride, value)
-    a.key_cache, a.value_cache = _ptr(key_cache), _ptr(value_cache)
-    _fill_strides(a.k_stride, key_cache)
-    _fill_strides(a.v_stride, value_cache)
+    return shape
 
 
 def paged_kv_write(key_cache: torch.Tensor, value_cache: torch.Tensor, key: torch.Tensor,
@@ -764,20 +775,22 @@ def paged_kv_write(key_cache: torch.Tensor, value_cache: torch.Tensor, key: torc
     to slots ``slot_mapping`` (int64 ``[N]``: block * block_size + slot in the
     block; negative: not written).  8-bit caches get the nearest code of
     ``x / scale``, saturating; see ``paged_kv_write`` in the header."""
-    _cuda(key_cache, "key_cache")
-    dev = _same_device(key_cache, (value_cache, "value_cache"), (key, "key"), (value, "value"),
-                       (slot_mapping, "slot_mapping"), (err_flag, "err_flag"))
-    a = CacheWriteArgs()
-    _cache_io_args(a, key, value, ("key", "value"), key_cache, value_cache, kv_cache_dtype,
-                   k_scale, v_scale)
-    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (key.shape[0],):
+    dev = _cuda_index(key_cache, "key_cache")
+    _one_device(dev, ((value_cache, "value_cache"), (key, "key"), (value, "value"),
+                      (slot_mapping, "slot_mapping"), (err_flag, "err_flag")))
+    nb, hk, dx, bs, x = _check_cache_io(key, value, ("key", "value"), key_cache, value_cache)
+    code = _kv_cache_code(key_cache, value_cache, key, kv_cache_dtype)
+    n = key.shape[0]
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (n,):
         raise ValueError("slot_mapping must be int64 [N]")
     if err_flag is not None and err_flag.dtype != torch.int32:
         raise ValueError("err_flag must be int32")
-    a.key, a.value = _ptr(key), _ptr(value)
-    a.slot_mapping, a.slot_stride = _ptr(slot_mapping), slot_mapping.stride(0)
-    a.err_flag = _ptr(err_flag)
-    _call_on(dev, stream, "paged_kv_write", lambda s: lib().paged_kv_write(ctypes.byref(a), s))
+    args = _PACK_WRITE.pack(n, hk, dx * x, bs, x, nb, _DTYPE_CODE[key.dtype], code, k_scale, v_scale,
+                            key.data_ptr(), *key.stride(), value.data_ptr(), *value.stride(),
+                            key_cache.data_ptr(), *key_cache.stride(), value_cache.data_ptr(),
+                            *value_cache.stride(), slot_mapping.data_ptr(), slot_mapping.stride(0),
+                            0 if err_flag is None else err_flag.data_ptr())
+    _call_on(dev, stream, "paged_kv_write", lib().paged_kv_write, args)
 
 
 def paged_kv_read(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: torch.Tensor,
@@ -790,50 +803,52 @@ def paged_kv_read(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: tor
     """Read tokens ``seq_starts[s] .. + cu_seq_lens[s+1] - cu_seq_lens[s]`` of every
     sequence back into ``key_out`` / ``value_out [N, num_kv_heads, head_size]``,
     packed at ``cu_seq_lens`` (int32 ``[B + 1]``), 8-bit codes as ``code * scale``."""
-    _cuda(key_cache, "key_cache")
-    dev = _same_device(key_cache, (value_cache, "value_cache"), (key_out, "key_out"),
-                       (value_out, "value_out"), (block_tables, "block_tables"),
-                       (cu_seq_lens, "cu_seq_lens"), (seq_starts, "seq_starts"),
-                       (kv_indptr, "kv_indptr"), (err_flag, "err_flag"))
-    a = CacheReadArgs()
-    _cache_io_args(a, key_out, value_out, ("key_out", "value_out"), key_cache, value_cache,
-                   kv_cache_dtype, k_scale, v_scale)
+    dev = _cuda_index(key_cache, "key_cache")
+    _one_device(dev, ((value_cache, "value_cache"), (key_out, "key_out"), (value_out, "value_out"),
+                      (block_tables, "block_tables"), (cu_seq_lens, "cu_seq_lens"),
+                      (seq_starts, "seq_starts"), (kv_indptr, "kv_indptr"), (err_flag, "err_flag")))
+    nb, hk, dx, bs, x = _check_cache_io(key_out, value_out, ("key_out", "value_out"), key_cache,
+                                        value_cache)
+    code = _kv_cache_code(key_cache, value_cache, key_out, kv_cache_dtype)
     for t, n in ((block_tables, "block_tables"), (cu_seq_lens, "cu_seq_lens"),
                  (seq_starts, "seq_starts"), (kv_indptr, "kv_indptr"), (err_flag, "err_flag")):
         if t is not None and t.dtype != torch.int32:
             raise ValueError(f"{n} must be int32")
-    a.num_seqs = cu_seq_lens.numel() - 1
-    _check_rows(cu_seq_lens, "cu_seq_lens", a.num_seqs + 1)
-    _check_rows(seq_starts, "seq_starts", a.num_seqs)
-    _fill_tables(a, block_tables, kv_indptr, max_blocks_per_seq)
-    a.key_out, a.value_out = _ptr(key_out), _ptr(value_out)
-    a.cu_seq_lens, a.seq_starts = _ptr(cu_seq_lens), _ptr(seq_starts)
-    a.err_flag = _ptr(err_flag)
-    _call_on(dev, stream, "paged_kv_read", lambda s: lib().paged_kv_read(ctypes.byref(a), s))
+    seqs = cu_seq_lens.numel() - 1
+    _check_rows(cu_seq_lens, "cu_seq_lens", seqs + 1)
+    _check_rows(seq_starts, "seq_starts", seqs)
+    cols, s0, s1 = _table_layout(block_tables, kv_indptr, max_blocks_per_seq, seqs)
+    args = _PACK_READ.pack(seqs, key_out.shape[0], hk, dx * x, bs, x, nb, cols,
+                           _DTYPE_CODE[key_out.dtype], code, k_scale, v_scale,
+                           key_out.data_ptr(), *key_out.stride(), value_out.data_ptr(),
+                           *value_out.stride(), key_cache.data_ptr(), *key_cache.stride(),
+                           value_cache.data_ptr(), *value_cache.stride(), block_tables.data_ptr(),
+                           s0, s1, _ptr(kv_indptr) or 0, cu_seq_lens.data_ptr(),
+                           _ptr(seq_starts) or 0, _ptr(err_flag) or 0)
+    _call_on(dev, stream, "paged_kv_read", lib().paged_kv_read, args)
 
 
 def _check_rows(t: Optional[torch.Tensor], name: str, n: int) -> None:
-    if t is not None and (n < 0 or tuple(t.shape) != (n,) or not t.is_contiguous()):
+    if t is not None and (t.shape != (n,) or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous [{max(n, 1)}] tensor")
 
 
-def _fill_tables(a, block_tables, kv_indptr, max_blocks_per_seq) -> None:
-    """Block-table fields: a 2-D table, or the flat page list of ``kv_indptr``."""
+def _table_layout(block_tables, kv_indptr, max_blocks_per_seq, num_seqs):
+    """(max_blocks_per_seq, strides) of a 2-D table, or of the flat page list of ``kv_indptr``."""
     if kv_indptr is None:
-        if block_tables.dim() != 2 or block_tables.shape[0] < a.num_seqs:
+        if block_tables.dim() != 2 or block_tables.shape[0] < num_seqs:
             raise ValueError("block_tables must be 2-D [num_seqs, max_blocks_per_seq]")
         cols = block_tables.shape[1]
-        a.max_blocks_per_seq = cols if max_blocks_per_seq is None else int(max_blocks_per_seq)
-        if a.max_blocks_per_seq > cols:
-            raise ValueError("max_blocks_per_seq exceeds block_tables' columns")
-        _fill_strides(a.bt_stride, block_tables)
-    else:
-        if block_tables.dim() != 1:
-            raise ValueError("with kv_indptr, block_tables is the flat page list (1-D)")
-        _check_rows(kv_indptr, "kv_indptr", a.num_seqs + 1)
-        a.bt_stride[0], a.bt_stride[1] = 0, block_tables.stride(0)
-        a.kv_indptr = _ptr(kv_indptr)
-    a.block_tables = _ptr(block_tables)
+        if max_blocks_per_seq is not None:
+            if max_blocks_per_seq > cols:
+                raise ValueError("max_blocks_per_seq exceeds block_tables' columns")
+            cols = int(max_blocks_per_seq)
+        s0, s1 = block_tables.stride()
+        return cols, s0, s1
+    if block_tables.dim() != 1:
+        raise ValueError("with kv_indptr, block_tables is the flat page list (1-D)")
+    _check_rows(kv_indptr, "kv_indptr", num_seqs + 1)
+    return 0, 0, block_tables.stride(0)
 
 
 def tree_workspace_bytes(head_size: int) -> int:
@@ -863,46 +878,58 @@ def paged_attention_tree(out: torch.Tensor, query: torch.Tensor, key_cache: torc
     position being ``positions[row]`` (int32) or its place in the sequence.
     ``workspace``: ``tree_workspace_bytes(head_size)`` bytes, one for each call
     that may run at the same time."""
-    _cuda(query, "query")
-    dev = _same_device(query, (out, "out"), (key_cache, "key_cache"), (value_cache, "value_cache"),
-                       (block_tables, "block_tables"), (seq_lens, "seq_lens"),
-                       (cu_query_lens, "cu_query_lens"), (workspace, "workspace"),
-                       (tree_mask, "tree_mask"), (positions, "positions"),
-                       (kv_indptr, "kv_indptr"), (err_flag, "err_flag"),
-                       (alibi_slopes, "alibi_slopes"))
-    if out.dtype != query.dtype or tuple(out.shape) != tuple(query.shape):
+    dev = _cuda_index(query, "query")
+    _one_device(dev, ((out, "out"), (key_cache, "key_cache"), (value_cache, "value_cache"),
+                      (block_tables, "block_tables"), (seq_lens, "seq_lens"),
+                      (cu_query_lens, "cu_query_lens"), (workspace, "workspace"),
+                      (tree_mask, "tree_mask"), (positions, "positions"), (kv_indptr, "kv_indptr"),
+                      (err_flag, "err_flag"), (alibi_slopes, "alibi_slopes")))
+    shape = query.shape
+    if out.dtype != query.dtype or out.shape != shape:
         raise ValueError("out must match query's shape and dtype")
-    for t, n in ((cu_query_lens, "cu_query_lens"), (positions, "positions")):
+    if query.dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {query.dtype}")
+    if query.dim() != 3 or key_cache.dim() != 5 or value_cache.dim() != 4:
+        raise ValueError("expected query [N,H,D], key_cache [NB,Hk,D/x,bs,x], value_cache [NB,Hk,D,bs]")
+    code = _kv_cache_code(key_cache, value_cache, query, kv_cache_dtype)
+    rows, heads, head_size = shape
+    nb, hk, dx, bs, x = key_cache.shape
+    if value_cache.shape != (nb, hk, head_size, bs) or dx * x != head_size:
+        raise ValueError("query, key_cache and value_cache do not belong together")
+    for t, n in ((block_tables, "block_tables"), (seq_lens, "seq_lens"),
+                 (cu_query_lens, "cu_query_lens"), (positions, "positions"), (kv_indptr, "kv_indptr"),
+                 (err_flag, "err_flag")):
         if t is not None and t.dtype != torch.int32:
             raise ValueError(f"{n} must be int32")
-    a = _decode_args(query, key_cache, value_cache, block_tables, seq_lens, scale, kv_indptr,
-                     err_flag, max_blocks_per_seq, kv_cache_dtype, k_scale, v_scale, alibi_slopes)
-    n = query.shape[0]
-    a.num_seqs = seq_lens.numel()
-    _check_rows(seq_lens, "seq_lens", a.num_seqs)
-    _check_rows(cu_query_lens, "cu_query_lens", a.num_seqs + 1)
-    _check_rows(positions, "positions", n)
-    if tuple(value_cache.shape) != (key_cache.shape[0], key_cache.shape[1], query.shape[2],
-                                    key_cache.shape[3]) or \
-            key_cache.shape[2] * key_cache.shape[4] != query.shape[2]:
-        raise ValueError("query, key_cache and value_cache do not belong together")
-    _fill_tables(a, block_tables, kv_indptr, max_blocks_per_seq)
-    t = TreeArgs()
-    t.num_tokens = n
-    t.cu_query_lens, t.positions = _ptr(cu_query_lens), _ptr(positions)
+    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32 or
+                                     not alibi_slopes.is_contiguous() or
+                                     alibi_slopes.shape != (heads,)):
+        raise ValueError("alibi_slopes must be a contiguous float32 [num_heads] tensor")
+    seqs = seq_lens.numel()
+    _check_rows(seq_lens, "seq_lens", seqs)
+    _check_rows(cu_query_lens, "cu_query_lens", seqs + 1)
+    _check_rows(positions, "positions", rows)
+    cols, s0, s1 = _table_layout(block_tables, kv_indptr, max_blocks_per_seq, seqs)
+    mask_ptr = mask_cols = m0 = m1 = 0
     if tree_mask is not None:
         if tree_mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError("tree_mask must be bool or uint8")
-        if tree_mask.dim() != 2 or tree_mask.shape[0] != n:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != rows:
             raise ValueError("tree_mask must be [num_tokens, columns]")
-        t.mask_cols = tree_mask.shape[1]
+        mask_cols = tree_mask.shape[1]
+        m0, m1 = tree_mask.stride()
         # a mask without columns hides every drafted token; its pointer may be null
-        t.tree_mask = _ptr(tree_mask) or _ptr(query)
-        _fill_strides(t.mask_stride, tree_mask)
-    t.logits_soft_cap = float(logits_soft_cap)
+        mask_ptr = tree_mask.data_ptr() or query.data_ptr()
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    t.workspace, t.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    os_ = _I64x3(*out.stride())
-    _call_on(dev, stream, "paged_attention_tree",
-             lambda s: lib().paged_attention_tree(_ptr(out), os_, ctypes.byref(a), ctypes.byref(t), s))
+    args = _PACK_DECODE.pack(seqs, heads, hk, head_size, bs, x, cols, nb, _DTYPE_CODE[query.dtype],
+                             scale, query.data_ptr(), *query.stride(), key_cache.data_ptr(),
+                             *key_cache.stride(), value_cache.data_ptr(), *value_cache.stride(),
+                             block_tables.data_ptr(), s0, s1, _ptr(kv_indptr) or 0,
+                             seq_lens.data_ptr(), _ptr(err_flag) or 0, code, k_scale, v_scale,
+                             _ptr(alibi_slopes) or 0, 0)
+    tree = _PACK_TREE.pack(rows, mask_cols, cu_query_lens.data_ptr(), mask_ptr, m0, m1,
+                           _ptr(positions) or 0, logits_soft_cap, workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size())
+    _call_on(dev, stream, "paged_attention_tree", lib().paged_attention_tree, out.data_ptr(),
+             _I64x3(*out.stride()), args, tree)

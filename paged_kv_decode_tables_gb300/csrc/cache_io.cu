@@ -88,87 +88,111 @@ __device__ __forceinline__ T from_cache(KV c, float scale) {
 
 // ------------------------------------------------------------------- write --
 
-constexpr int kWTokens = 32;    // tokens of a CTA
-constexpr int kWThreads = 128;
+constexpr int kWSide = 128;            // threads on the keys, and as many on the values
+constexpr int kWThreads = 2 * kWSide;
 
-// CTA (x, h): tokens 32 x .. 32 x + 31 of kv head h.  Warp 0 cuts the tile into
-// groups of up to 8 consecutive slots that do not cross a multiple of 8; a
-// group of 8 is written 8 tokens at a time (a prompt), shorter ones token by
-// token (decode steps: every token goes to a page of its own).
-template <typename T, typename KV, bool VEC>
+// CTA (x, h): TOK tokens of kv head h, half of its warps on the keys and half on
+// the values.  The tile's tokens are cut into groups of up to 8 consecutive
+// slots that do not cross a multiple of 8: a group of 8 is a block of 8 tokens
+// x 8 dims that is written 8 tokens at a time (a prompt), shorter ones go token
+// by token (decode steps: every token has a page of its own).
+template <typename T, typename KV, bool VEC, int TOK>
 __global__ void __launch_bounds__(kWThreads) cache_write_kernel(const CacheWriteParams p) {
   constexpr int X = 16 / int(sizeof(KV));
-  __shared__ int64_t page_k[kWTokens], page_v[kWTokens];  // element offset of the token's page
-  __shared__ int slot_of[kWTokens];                       // slot in the page, -1: not written
-  __shared__ int group_first[kWTokens], group_size[kWTokens];
-  __shared__ int num_groups;
+  __shared__ int64_t slots[TOK];                  // -1: not written
+  __shared__ int64_t page_k[TOK], page_v[TOK];    // element offset of the token's page
+  __shared__ int slot_of[TOK];                    // slot in the page, -1: not written
+  __shared__ int group_first[TOK], group_size[TOK];
+  __shared__ int heads_of_warp[2];
   const int tid = threadIdx.x, D = p.head_size, BS = p.block_size, h = blockIdx.y;
-  const int64_t i0 = int64_t(blockIdx.x) * kWTokens;
+  const int64_t i0 = int64_t(blockIdx.x) * TOK;
   grid_dependency_wait();
   allow_dependent_launch();
-  if (tid < kWTokens) {
-    int64_t slot = -1;
+  int64_t slot = -1;
+  if (tid < TOK) {
     if (i0 + tid < p.num_tokens) slot = p.slots[(i0 + tid) * p.slot_stride];
     if (slot >= p.num_slots) {
       flag_error(p.err, PKV_ERRF_BLOCK_ID);
       slot = -1;
     }
+    if (slot < 0) slot = -1;
     const int64_t blk = slot < 0 ? 0 : slot / BS;
     page_k[tid] = blk * p.kc_s0 + int64_t(h) * p.kc_s1;
     page_v[tid] = blk * p.vc_s0 + int64_t(h) * p.vc_s1;
     slot_of[tid] = slot < 0 ? -1 : int(slot - blk * BS);
-    const int64_t prev = __shfl_up_sync(kFull, slot, 1);
-    const bool head = slot >= 0 && (tid == 0 || slot != prev + 1 || slot % 8 == 0 || prev < 0);
-    const unsigned heads = __ballot_sync(kFull, head);
-    const unsigned breaks = heads | __ballot_sync(kFull, slot < 0);
-    if (head) {
-      const int g = __popc(heads & ((1u << tid) - 1u));
-      const unsigned later = tid == 31 ? 0u : breaks >> (tid + 1);
-      group_first[g] = tid;
-      group_size[g] = later ? __ffs(later) : kWTokens - tid;
-    }
-    if (tid == 0) num_groups = __popc(heads);
+    slots[tid] = slot;
   }
   __syncthreads();
-  const T *key = static_cast<const T *>(p.key) + int64_t(h) * p.k_s1;
-  const T *value = static_cast<const T *>(p.value) + int64_t(h) * p.v_s1;
-  KV *kc = static_cast<KV *>(p.key_cache), *vc = static_cast<KV *>(p.value_cache);
-  // keys: chunks of a token across lanes, so rows are read whole
-  const int chunks = D / X;
-  for (int i = tid; i < kWTokens * chunks; i += kWThreads) {
-    const int t = i / chunks, c = i - t * chunks;
-    if (slot_of[t] < 0) continue;
-    alignas(16) T x[X];
-    alignas(16) KV q[X];
-    load_elems<T, X, VEC>(key + (i0 + t) * p.k_s0 + c * X, x);
-#pragma unroll
-    for (int e = 0; e < X; ++e) q[e] = to_cache<T, KV>(x[e], p.k_scale);
-    store_elems<KV, X, true>(kc + page_k[t] + (int64_t(c) * BS + slot_of[t]) * X, q);
+  bool head = false;
+  unsigned heads = 0;
+  if (tid < (TOK + 31) / 32 * 32) {
+    head = slot >= 0 && (tid == 0 || slots[tid - 1] != slot - 1 || slot % 8 == 0);
+    heads = __ballot_sync(kFull, head);
+    if ((tid & 31) == 0) heads_of_warp[tid >> 5] = __popc(heads);
   }
-  // values: (group, 8 dims) blocks
-  const int cols = D / 8;
-  const int ng = num_groups;
-  for (int i = tid; i < ng * cols; i += kWThreads) {
-    const int g = i / cols, d = (i - g * cols) * 8;
-    const int t0 = group_first[g], n = group_size[g];
-    KV *dst = vc + page_v[t0] + int64_t(d) * BS + slot_of[t0];
-    if (n == 8) {
-      alignas(16) KV b[8][8];  // [dim][token]
+  __syncthreads();
+  if (head) {
+    const int g = (tid >= 32 ? heads_of_warp[0] : 0) + __popc(heads & ((1u << (tid & 31)) - 1u));
+    int n = 1;
+    while (tid + n < TOK && slots[tid + n] == slot + n && (slot + n) % 8 != 0) ++n;
+    group_first[g] = tid;
+    group_size[g] = n;
+  }
+  const int ng = heads_of_warp[0] + (TOK > 32 ? heads_of_warp[1] : 0);
+  __syncthreads();
+  if (tid < kWSide) {
+    // values: (group, 8 dims) blocks
+    const T *value = static_cast<const T *>(p.value) + int64_t(h) * p.v_s1;
+    KV *vc = static_cast<KV *>(p.value_cache);
+    const int shift = 31 - __clz(D / 8);
+    for (int i = tid; i < ng << shift; i += kWSide) {
+      const int g = i >> shift, d = (i - (g << shift)) * 8;
+      const int t0 = group_first[g], n = group_size[g];
+      KV *dst = vc + page_v[t0] + int64_t(d) * BS + slot_of[t0];
+      if (n == 8) {
+        alignas(16) T x[8][8];   // [token][dim]
+        alignas(16) KV b[8][8];  // [dim][token]
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        alignas(16) T x[8];
-        load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x);
+        for (int t = 0; t < 8; ++t)
+          load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x[t]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) b[e][t] = to_cache<T, KV>(x[e], p.v_scale);
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) b[e][t] = to_cache<T, KV>(x[t][e], p.v_scale);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) store_elems<KV, 8, true>(dst + e * BS, b[e]);
+      } else {
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+          alignas(16) T x[8];
+          load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e * BS + t] = to_cache<T, KV>(x[e], p.v_scale);
+        }
+      }
+    }
+  } else {
+    // keys: chunks of a token across lanes, so rows are read whole; four loads in flight
+    const T *key = static_cast<const T *>(p.key) + int64_t(h) * p.k_s1;
+    KV *kc = static_cast<KV *>(p.key_cache);
+    const int shift = 31 - __clz(D / X);
+    constexpr int U = 4;
+    for (int i = tid - kWSide; i < TOK << shift; i += U * kWSide) {
+      alignas(16) T x[U][X];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = i + u * kWSide, t = j >> shift, c = j - (t << shift);
+        if (t < TOK && slot_of[t] >= 0)
+          load_elems<T, X, VEC>(key + (i0 + t) * p.k_s0 + c * X, x[u]);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) store_elems<KV, 8, true>(dst + e * BS, b[e]);
-    } else {
-      for (int t = 0; t < n; ++t) {
-        alignas(16) T x[8];
-        load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x);
+      for (int u = 0; u < U; ++u) {
+        const int j = i + u * kWSide, t = j >> shift, c = j - (t << shift);
+        if (t >= TOK || slot_of[t] < 0) continue;
+        alignas(16) KV q[X];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dst[e * BS + t] = to_cache<T, KV>(x[e], p.v_scale);
+        for (int e = 0; e < X; ++e) q[e] = to_cache<T, KV>(x[u][e], p.k_scale);
+        store_elems<KV, X, true>(kc + page_k[t] + (int64_t(c) * BS + slot_of[t]) * X, q);
       }
     }
   }
@@ -267,12 +291,22 @@ __global__ void __launch_bounds__(kRThreads) cache_read_kernel(const CacheReadPa
 
 // ------------------------------------------------------------------ launch --
 
+// Tokens of a CTA: 64 (a prompt's tiles), or 16 where that leaves fewer than 512
+// CTAs (decode steps: 512 tokens x 8 kv heads in E4M3 would be 64 CTAs whose
+// threads write 64 bytes one by one eight times over).
+template <typename T, typename KV, bool VEC>
+cudaError_t write_vec(const CacheWriteParams &p, cudaStream_t s) {
+  const int64_t tiles = (int64_t(p.num_tokens) + 63) / 64;
+  if (tiles * p.num_kv_heads >= 512)
+    return launch_programmatic(cache_write_kernel<T, KV, VEC, 64>, dim3(tiles, p.num_kv_heads),
+                               dim3(kWThreads), 0, s, p);
+  return launch_programmatic(cache_write_kernel<T, KV, VEC, 16>,
+                             dim3((p.num_tokens + 15) / 16, p.num_kv_heads), dim3(kWThreads), 0, s, p);
+}
+
 template <typename T, typename KV>
 cudaError_t write_as(const CacheWriteParams &p, bool vec, cudaStream_t s) {
-  const dim3 grid((int64_t(p.num_tokens) + kWTokens - 1) / kWTokens, p.num_kv_heads);
-  if (vec)
-    return launch_programmatic(cache_write_kernel<T, KV, true>, grid, dim3(kWThreads), 0, s, p);
-  return launch_programmatic(cache_write_kernel<T, KV, false>, grid, dim3(kWThreads), 0, s, p);
+  return vec ? write_vec<T, KV, true>(p, s) : write_vec<T, KV, false>(p, s);
 }
 
 template <typename T, typename KV>
