@@ -59,20 +59,36 @@ __device__ __forceinline__ void store_elems(E *p, const E (&v)[N]) {
   }
 }
 
-// x / scale as a code of the cache (or x itself).
-template <typename T, typename KV>
-__device__ __forceinline__ KV to_cache(T x, float scale) {
-  if constexpr (is_fp8<KV>::value) {
-    const float q = __fdiv_rn(to_f32<T>(x), scale);
-    uint16_t r;
-    if constexpr (std::is_same<KV, fp8_e4m3_t>::value)
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(q));
-    else
-      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(q));
-    return KV{uint8_t(r)};
-  } else {
-    return x;
+// x / scale in fp32, correctly rounded.  DIV: by a division; else, for scales in
+// [2^-60, 2^60], by Markstein's correction of the product with the rounded
+// reciprocal (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): with inv = RN(1 / scale), q = RN(x inv) and the
+// exact remainder c = x - q scale, RN(q + c inv) = RN(x / scale).  Three
+// instructions instead of about ten; the divisions bound the copy.  A quotient
+// beyond 10^30 saturates in the code either way, and one below 10^-30 is far
+// below half of the smallest code (and keeps the sign of a zero).
+template <bool DIV>
+struct Quotient {
+  float scale, inv;
+  __device__ __forceinline__ explicit Quotient(float s) : scale(s), inv(1.f / s) {}
+  __device__ __forceinline__ float operator()(float x) const {
+    if constexpr (DIV) return __fdiv_rn(x, scale);
+    const float q = x * inv;
+    const float r = fmaf(fmaf(-q, scale, x), inv, q);
+    return fabsf(q) > 1e-30f && fabsf(q) < 1e30f ? r : q;
   }
+};
+
+// Two elements as codes of the cache, the first in the low byte.
+template <typename T, typename KV, bool DIV>
+__device__ __forceinline__ uint32_t to_codes2(T a, T b, const Quotient<DIV> &by) {
+  const float x = by(to_f32<T>(a)), y = by(to_f32<T>(b));
+  uint16_t r;
+  if constexpr (std::is_same<KV, fp8_e4m3_t>::value)
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+  else
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+  return r;
 }
 
 template <typename T, typename KV>
@@ -96,7 +112,7 @@ constexpr int kWThreads = 2 * kWSide;
 // slots that do not cross a multiple of 8: a group of 8 is a block of 8 tokens
 // x 8 dims that is written 8 tokens at a time (a prompt), shorter ones go token
 // by token (decode steps: every token has a page of its own).
-template <typename T, typename KV, bool VEC, int TOK>
+template <typename T, typename KV, bool VEC, int TOK, bool DIV>
 __global__ void __launch_bounds__(kWThreads) cache_write_kernel(const CacheWriteParams p) {
   constexpr int X = 16 / int(sizeof(KV));
   __shared__ int64_t slots[TOK];                  // -1: not written
@@ -145,30 +161,51 @@ __global__ void __launch_bounds__(kWThreads) cache_write_kernel(const CacheWrite
     const T *value = static_cast<const T *>(p.value) + int64_t(h) * p.v_s1;
     KV *vc = static_cast<KV *>(p.value_cache);
     const int shift = 31 - __clz(D / 8);
+    const Quotient<DIV> by(p.v_scale);
     for (int i = tid; i < ng << shift; i += kWSide) {
       const int g = i >> shift, d = (i - (g << shift)) * 8;
       const int t0 = group_first[g], n = group_size[g];
       KV *dst = vc + page_v[t0] + int64_t(d) * BS + slot_of[t0];
-      if (n == 8) {
-        alignas(16) T x[8][8];   // [token][dim]
-        alignas(16) KV b[8][8];  // [dim][token]
+      alignas(16) T x[8][8];  // [token][dim]
+      if constexpr (!is_fp8<KV>::value) {
+        if (n == 8) {
+          alignas(16) KV b[8][8];  // [dim][token]
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-          load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x[t]);
+          for (int t = 0; t < 8; ++t)
+            load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x[t]);
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+          for (int t = 0; t < 8; ++t)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) b[e][t] = to_cache<T, KV>(x[t][e], p.v_scale);
+            for (int e = 0; e < 8; ++e) b[e][t] = x[t][e];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) store_elems<KV, 8, true>(dst + e * BS, b[e]);
-      } else {
-#pragma unroll 1
-        for (int t = 0; t < n; ++t) {
-          alignas(16) T x[8];
-          load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e * BS + t] = to_cache<T, KV>(x[e], p.v_scale);
+          for (int e = 0; e < 8; ++e) store_elems<KV, 8, true>(dst + e * BS, b[e]);
+          continue;
         }
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (t < n) load_elems<T, 8, VEC>(value + (i0 + t0 + t) * p.v_s0 + d, x[t]);
+      if constexpr (is_fp8<KV>::value) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) w[t] = to_codes2<T, KV, DIV>(x[2 * t][e], x[2 * t + 1][e], by);
+          if (n == 8) {
+            *reinterpret_cast<uint2 *>(dst + e * BS) =
+                make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 7; ++t)
+              if (t < n) dst[e * BS + t].bits = uint8_t(w[t >> 1] >> (t & 1) * 8);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int t = 0; t < 7; ++t)
+            if (t < n) dst[e * BS + t] = x[t][e];
       }
     }
   } else {
@@ -176,6 +213,7 @@ __global__ void __launch_bounds__(kWThreads) cache_write_kernel(const CacheWrite
     const T *key = static_cast<const T *>(p.key) + int64_t(h) * p.k_s1;
     KV *kc = static_cast<KV *>(p.key_cache);
     const int shift = 31 - __clz(D / X);
+    const Quotient<DIV> by(p.k_scale);
     constexpr int U = 4;
     for (int i = tid - kWSide; i < TOK << shift; i += U * kWSide) {
       alignas(16) T x[U][X];
@@ -189,10 +227,16 @@ __global__ void __launch_bounds__(kWThreads) cache_write_kernel(const CacheWrite
       for (int u = 0; u < U; ++u) {
         const int j = i + u * kWSide, t = j >> shift, c = j - (t << shift);
         if (t >= TOK || slot_of[t] < 0) continue;
-        alignas(16) KV q[X];
+        KV *dst = kc + page_k[t] + (int64_t(c) * BS + slot_of[t]) * X;
+        if constexpr (is_fp8<KV>::value) {
+          uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < X; ++e) q[e] = to_cache<T, KV>(x[u][e], p.k_scale);
-        store_elems<KV, X, true>(kc + page_k[t] + (int64_t(c) * BS + slot_of[t]) * X, q);
+          for (int e = 0; e < 8; ++e) w[e] = to_codes2<T, KV, DIV>(x[u][2 * e], x[u][2 * e + 1], by);
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16,
+                                                       w[4] | w[5] << 16, w[6] | w[7] << 16);
+        } else {
+          store_elems<KV, X, true>(dst, x[u]);
+        }
       }
     }
   }
@@ -294,19 +338,25 @@ __global__ void __launch_bounds__(kRThreads) cache_read_kernel(const CacheReadPa
 // Tokens of a CTA: 64 (a prompt's tiles), or 16 where that leaves fewer than 512
 // CTAs (decode steps: 512 tokens x 8 kv heads in E4M3 would be 64 CTAs whose
 // threads write 64 bytes one by one eight times over).
-template <typename T, typename KV, bool VEC>
+template <typename T, typename KV, bool VEC, bool DIV>
 cudaError_t write_vec(const CacheWriteParams &p, cudaStream_t s) {
   const int64_t tiles = (int64_t(p.num_tokens) + 63) / 64;
   if (tiles * p.num_kv_heads >= 512)
-    return launch_programmatic(cache_write_kernel<T, KV, VEC, 64>, dim3(tiles, p.num_kv_heads),
+    return launch_programmatic(cache_write_kernel<T, KV, VEC, 64, DIV>, dim3(tiles, p.num_kv_heads),
                                dim3(kWThreads), 0, s, p);
-  return launch_programmatic(cache_write_kernel<T, KV, VEC, 16>,
-                             dim3((p.num_tokens + 15) / 16, p.num_kv_heads), dim3(kWThreads), 0, s, p);
+  return launch_programmatic(cache_write_kernel<T, KV, VEC, 16, DIV>,
+                             dim3((int64_t(p.num_tokens) + 15) / 16, p.num_kv_heads), dim3(kWThreads),
+                             0, s, p);
 }
 
 template <typename T, typename KV>
 cudaError_t write_as(const CacheWriteParams &p, bool vec, cudaStream_t s) {
-  return vec ? write_vec<T, KV, true>(p, s) : write_vec<T, KV, false>(p, s);
+  if constexpr (is_fp8<KV>::value) {
+    auto plain = [](float x) { return x >= 0x1p-60f && x <= 0x1p60f; };
+    if (!plain(p.k_scale) || !plain(p.v_scale))
+      return vec ? write_vec<T, KV, true, true>(p, s) : write_vec<T, KV, false, true>(p, s);
+  }
+  return vec ? write_vec<T, KV, true, false>(p, s) : write_vec<T, KV, false, false>(p, s);
 }
 
 template <typename T, typename KV>

@@ -130,6 +130,25 @@ def test_write_special_values(kv, dtype):
         assert torch.equal(a[ok], b[ok])
 
 
+@pytest.mark.parametrize("kv", ["fp8_e4m3", "fp8_e5m2"])
+@pytest.mark.parametrize("scale", [1.0, 0.25, 0.1, 3.0, 0.043, 0.0271, 7.3e-18, 1.1e18, 1.0 / 3.0, 7e-39, 2.0 ** -130, 3e38, 1.1754944e-38])
+def test_every_half_precision_value_and_scale(kv, scale):
+    """All fp16 numbers over scales that are powers of two, round to them, have
+    no normal reciprocal: the code is that of the fp32 quotient, ties included."""
+    n = 1024
+    key = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.float16).view(n, 1, 64).contiguous()
+    inp = _batch("f16", kv, 64, 16, 1, [n], 4)
+    kc, vc = inp["key_cache"].cuda(), inp["value_cache"].cuda()
+    slots = _slots(inp, [(0, 0, n)])
+    pkv.paged_kv_write(kc, vc, key.cuda(), key.cuda(), slots.cuda(), kv_cache_dtype=kv, k_scale=scale, v_scale=scale)
+    want = oracle.encode(key.float() / torch.tensor(scale, dtype=torch.float32), oracle.fp8.format_of(kv))
+    rows = kc.cpu().permute(0, 3, 1, 2, 4).reshape(-1, 1, 64)[slots], vc.cpu().permute(0, 3, 1, 2).reshape(-1, 1, 64)[slots]
+    nan = torch.isnan(key)
+    for got in rows:
+        assert torch.equal(got[~nan], want[~nan])
+        assert bool(torch.isnan(oracle.fp8.decode(got[nan], oracle.fp8.format_of(kv))).all())
+
+
 @pytest.mark.parametrize("dtype,kv,D,bs,Hk", CASES)
 @pytest.mark.parametrize("start", [0, 1, 13])
 def test_read(dtype, kv, D, bs, Hk, start):
