@@ -227,8 +227,8 @@ pkv_status_t pkv_set_wait_limit_ns(uint64_t ns);
 
 /*
  * Test hook for the timeout path above, one-shot: every stage of the NEXT
- * attention launch (paged_attention_decode or paged_attention_v2_partition, in
- * any thread) expects `bytes` (a multiple of 16, at most 65536) more than its
+ * attention launch (paged_attention_decode, paged_attention_v2_partition, or
+ * paged_attention_tree with 16-bit queries, in any thread) expects `bytes` (a multiple of 16, at most 65536) more than its
  * copies deliver, so each of its waits runs into the limit.  That launch
  * clears the hook; later launches are unaffected.  0 clears it without a
  * launch.  Only for exercising failure detection.
@@ -594,7 +594,8 @@ size_t pkv_cache_write_args_size(void);
  *   block_tables, bt_stride, kv_indptr, max_blocks_per_seq, num_blocks: as for
  *       paged_attention_decode.
  *   cu_seq_lens: [num_seqs + 1] int32, not descending, starting at 0; a row that
- *       descends or leaves [0, num_tokens] is skipped and sets PKV_ERRF_INDPTR.
+ *       descends or leaves [0, num_tokens] is skipped and sets PKV_ERRF_INDPTR
+ *       (what else a batch with such a row writes is unspecified, within its rows).
  *   seq_starts: optional [num_seqs] int32.  Tokens before 0 or past the row's
  *       pages are not written and set PKV_ERRF_SEQ_LEN.
  * Types and sizes as for paged_kv_write.  num_seqs <= 65535.
@@ -668,7 +669,10 @@ size_t pkv_cache_read_args_size(void);
  *       256-byte boundary, for the partial results of sequences that several
  *       CTAs share.  Its size depends on the GPU and the head size only.  Nothing
  *       in it outlives the call; calls that overlap on the GPU need one each.
- * K and V are read once per 128 query rows of a kv head (fp32: 32).
+ * K and V are read once per 128 query rows of a kv head (fp32: 32).  A value of a
+ * token before the drafted ones that is not finite makes its dim of every row
+ * of the kv head NaN or infinite.  Every wait is bounded (pkv_set_wait_limit_ns;
+ * PKV_ERRF_TIMEOUT).
  * Types, sizes and errors as for paged_attention_decode.
  */
 typedef struct {

@@ -88,9 +88,11 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s, bool fla
       cap_pages = 0;
     }
   }
-  if (L < 0 || int64_t(L) > cap_pages * p.block_size) {
+  // (token numbers plus a tile stay within 31 bits)
+  const int64_t most = min(cap_pages * p.block_size, int64_t(0x7fffff00));
+  if (L < 0 || int64_t(L) > most) {
     if (flag) flag_error(p.err, PKV_ERRF_SEQ_LEN);
-    L = L < 0 ? 0 : int(cap_pages * p.block_size);
+    L = L < 0 ? 0 : int(most);
   }
   int T = 0;
   if (q0 < 0 || q1 < q0 || q1 > p.num_tokens) {

@@ -48,6 +48,13 @@
 
 namespace pkv {
 
+// L2 policy without preference, for pages that other CTAs read as well.
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
 // Registers per thread of a group of four warps, up or down.
 template <int N>
 __device__ __forceinline__ void reg_alloc() {

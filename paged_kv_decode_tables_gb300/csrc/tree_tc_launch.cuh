@@ -15,6 +15,16 @@ pkv_status_t launch_tree_tc_kernel(const TreeParams &p, int ctas, cudaStream_t s
   using Cfg = TreeTcCfg<T, KV, D, BS>;
   static std::atomic<unsigned long long> done{0};
   auto kernel = tree_tc_kernel<T, KV, D, BS, BIASED>;
+  if constexpr (Cfg::NWG == 2) {
+    // The kernel deals its launch registers out anew; compiled to fewer than it
+    // deals out (they come in eights) its warps would wait for the rest forever.
+    static const bool enough = [&] {
+      cudaFuncAttributes a = {};
+      return cudaFuncGetAttributes(&a, kernel) == cudaSuccess &&
+             (a.numRegs + 7) / 8 * 8 * 4 >= 2 * Cfg::kSoftRegs + Cfg::kPrepRegs + Cfg::kIssueRegs;
+    }();
+    if (!enough) return PKV_ERR_UNSUPPORTED;
+  }
   if (!ensure_smem_attr(kernel, Cfg::kSmem, done)) return PKV_ERR_CUDA;
   return launch_programmatic(kernel, dim3(ctas), dim3(Cfg::kThreads), Cfg::kSmem, stream, p) ==
                  cudaSuccess

@@ -303,6 +303,36 @@ def test_bad_device_data_is_flagged(dtype, kv):
     assert e == pkv.PKV_ERRF_INDPTR and torch.equal(out[4:], good[4:])
 
 
+@pytest.mark.parametrize("dtype,kv", [("bf16", "auto"), ("bf16", "fp8_e4m3"), ("f32", "auto")])
+def test_no_drafted_tokens_at_all(dtype, kv):
+    inp = _batch(dtype, kv, 128, 16, 4, 2, [100, 3], [0, 0], 20, mask=None)
+    inp["query"] = torch.zeros(5, 4, 128, dtype=DT[dtype])
+    out = torch.full((5, 4, 128), 3.0, dtype=DT[dtype], device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _run(inp, out=out, err=err)
+    assert bool((out == 3).all()) and int(err) == 0
+
+
+@pytest.mark.parametrize("kv", ["auto", "fp8_e4m3"])
+def test_a_copy_that_never_arrives_is_reported(kv):
+    """Every key stage of one launch expects 16 bytes more than arrive: its waits
+    run into the (short) limit, the launch ends and says so, the next one is right."""
+    inp = _batch("bf16", kv, 128, 16, 8, 2, [700, 40], [5, 3], 21)
+    good = _run(inp)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.set_wait_limit_ns(20_000_000)
+    try:
+        pkv._test_set_unarrived_bytes(16)
+        _run(inp, err=err)
+        torch.cuda.synchronize()
+    finally:
+        pkv._test_set_unarrived_bytes(0)
+        pkv.set_wait_limit_ns(0)
+    assert int(err) & pkv.PKV_ERRF_TIMEOUT
+    err.zero_()
+    assert torch.equal(_run(inp, err=err), good) and int(err) == 0
+
+
 def test_streams_graphs_and_shared_workspace():
     """Two captured graphs that share a workspace, replayed in turn; calls on two
     streams with a workspace each."""
