@@ -108,6 +108,7 @@ struct TreeTcCfg {
   static constexpr int MB = OS / 2;
   static_assert(OS % 2 == 0 && RS % 2 == 0, "key and value slots apart");
   static_assert(OS <= 16 && RS <= 16 && MB <= 8, "barrier arrays");
+  static constexpr int kSideWarps = kFp8 ? 2 : 4;  // prep warps on the values (and on 8-bit keys)
   static constexpr int kWords = TT / 32;        // mask words of a tile
   static constexpr int kSoftWarps = 4 * NWG;
     static constexpr int kThreads = (kSoftWarps + 8) * 32;
@@ -262,12 +263,12 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
   uint8_t *smem = tree_tc_smem;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff);
   uint64_t *raw_full = bars + 0;     // [RS <= 16] pages landed (tx bytes)
-  uint64_t *raw_free = bars + 16;    // [RS] 8-bit caches: widened (4 prep warps)
+  uint64_t *raw_free = bars + 16;    // [RS] 8-bit caches: widened (2 prep warps)
   uint64_t *op_free = bars + 32;     // [OS <= 16] MMAs on the slot done (commit)
   // Operands ready, by tile modulo 8 and not by slot (16-bit keys need no prep,
   // and with an odd number of slots a slot holds keys and values in turn).
-  uint64_t *k_ready = bars + 48;     // [8] 8-bit caches: keys widened (4 prep warps)
-  uint64_t *v_ready = bars + 56;     // [8] values in operand layout (4 prep warps)
+  uint64_t *k_ready = bars + 48;     // [8] 8-bit caches: keys widened (2 prep warps)
+  uint64_t *v_ready = bars + 56;     // [8] values in operand layout (2 or 4 prep warps)
   uint64_t *s_full = bars + 64;      // [NSB <= 4] scores in TMEM (commit)
   uint64_t *p_full = bars + 68;      // [NSB] probabilities written (4 warps)
   uint64_t *pv_done = bars + 72;     // [NSB] value product done (commit)
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
   uint64_t *q_free = bars + 85;      // last score MMA of the unit done (commit)
   uint64_t *o_free = bars + 86;      // accumulators read (softmax warps)
   uint64_t *stat_full = bars + 87;   // group sums exchanged (softmax warps)
-  uint64_t *prep_bar = bars + 88;    // the prep warps among themselves
+  uint64_t *prep_bar = bars + 88;    // the value prep warps among themselves
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 90);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 91);
   uint32_t *masks = reinterpret_cast<uint32_t *>(smem + Cfg::kMaskOff);  // [MB][128][kWords]
@@ -292,12 +293,12 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < RS; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_free[i], 4);
+      mbar_init(&raw_free[i], Cfg::kSideWarps);
     }
     for (int i = 0; i < OS; ++i) mbar_init(&op_free[i], 1);
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&k_ready[i], 4);
-      mbar_init(&v_ready[i], 4);
+      mbar_init(&k_ready[i], Cfg::kSideWarps);
+      mbar_init(&v_ready[i], Cfg::kSideWarps);
     }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&s_full[i], 1);
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
     }
     mbar_init(q_ready, 4);
     mbar_init(q_free, 1);
-    mbar_init(prep_bar, 4);
+    mbar_init(prep_bar, Cfg::kSideWarps);
     mbar_init(o_free, Cfg::kSoftWarps);
     mbar_init(stat_full, Cfg::kSoftWarps);
     for (int i = 0; i < Cfg::kUnits; ++i) {
@@ -671,6 +672,11 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
     if constexpr (NWG == 2) reg_dealloc<Cfg::kPrepRegs>();
     // -------------------------------------------------------------- prep --
     const int pt = threadIdx.x - kPrep0 * 32, pw = warp - kPrep0;
+    // 8-bit caches: two warps widen the keys, two the values (all four on one after
+    // the other: 111 us instead of 99 on two sequences of 32k tokens).
+    const int side = kFp8 ? pw >> 1 : 1;
+    constexpr int kSide = Cfg::kSideWarps, kSideThreads = 32 * kSide;
+    const int st = pt % kSideThreads, sw0 = pw % kSide;
     uint32_t g = 0;  // tiles
     uint32_t syncs = 0;
     for (int u = 0; !failed; ++u) {
@@ -761,8 +767,8 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
         const int nt = min(TT, d.L - t0);  // tokens of the tile (<= 0: none)
         const bool tail = t0 + TT > d.ctx;
         const uint32_t mb = g % MB;
-#pragma unroll 1
-        for (int kv = kFp8 ? 0 : 1; kv < 2; ++kv) {
+        {
+          const int kv = side;
           const uint32_t n = 2 * g + kv, rs = n % RS, os = n % OS;
           if (!wait_warp(&raw_full[rs], (n / RS) & 1u) ||
               (kFp8 && n >= uint32_t(OS) && !wait_warp(&op_free[os], (n / OS - 1) & 1u))) {
@@ -773,7 +779,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
           if constexpr (kFp8) {
             const uint8_t *raw = smem + Cfg::kRawOff + rs * Cfg::kRawTile;
 #pragma unroll 4
-            for (int i = pt; i < TT * D / 16; i += 128) {
+            for (int i = st; i < TT * D / 16; i += kSideThreads) {
               const uint4 w = *reinterpret_cast<const uint4 *>(raw + i * 16);
               uint32_t h[8];
               fp8x4_to_f16x2<KV>(w.x, h[0], h[1]);
@@ -824,7 +830,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
           }
           if (kv == 1 && tail) {
             // The warps' accesses to the same rows are apart from here on.
-            if (pt < 4) bad[mb * 4 + pt] = 0;
+            if (st < 4) bad[mb * 4 + st] = 0;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(prep_bar);
             if (!wait_warp(prep_bar, syncs++ & 1u)) {
@@ -832,7 +838,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
               break;
             }
             // What each row sees of the tile, a bit per token.
-            for (int i = pw; i < nodes; i += 4) {
+            for (int i = sw0; i < nodes; i += kSide) {
               const int node = node0 + i;
 #pragma unroll
               for (int w = 0; w < kWords; ++w) {
@@ -853,7 +859,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
             // NaN); such tokens are marked, and the rows that see one add its
             // values themselves.
             const int t8 = max(0, d.ctx - t0) / 8;  // 16-byte pieces: 8 tokens of a dim
-            for (int i = pt; i < (TT / 8 - t8) * D; i += 128) {
+            for (int i = st; i < (TT / 8 - t8) * D; i += kSideThreads) {
               const int t = (t8 + i / D) * 8, dim = i % D;
               const int sw = BS == 16 ? (dim >> 2) & 1 : (BS == 32 ? (dim >> 1) & 3 : 0);
               uint4 *e = reinterpret_cast<uint4 *>(op + t / BS * kPage + dim * BS * 2 +

@@ -129,7 +129,7 @@ def test_ragged_trees(dtype, kv, D, bs, H, Hk):
 
 
 @pytest.mark.parametrize("dtype,kv,D,bs,H,Hk", [CASES[i] for i in (0, 5, 10, 12, 3)])
-@pytest.mark.parametrize("cap,alibi", [(5.0, False), (0.0, True), (30.0, True)])
+@pytest.mark.parametrize("cap,alibi", [(5.0, False), (50.0, False), (0.0, True), (30.0, True)])
 def test_soft_cap_and_alibi(dtype, kv, D, bs, H, Hk, cap, alibi):
     lens, drafts = [400, 33, 9, 150], [5, 16, 9, 1]
     inp = _batch(dtype, kv, D, bs, H, Hk, lens, drafts, 3, alibi=alibi, peaky_fraction=0.02)
