@@ -10,7 +10,9 @@
 // end, are cut into equal runs, one per CTA, whatever the lengths are: a batch
 // of uneven sequences and a single long one both fill the GPU, and the
 // partial results are bounded by two per CTA (a run's first and last unit) --
-// the workspace depends on the GPU and the head size only.  A unit inside one
+// the workspace depends on the GPU and the head size only.  In the line a unit
+// has UC places in front of its tiles, for what it costs beside them; a run that
+// starts or ends in those starts or ends at the unit's first tile.  A unit inside one
 // run is written to `out` by its CTA; the others are joined by
 // tree_join_kernel from their partial sums (acc = sum 2^(x - m) v, l = sum
 // 2^(x - m), m; x in log2 units).
@@ -29,8 +31,8 @@ struct TreeCut {
   int32_t valid;
   int32_t q0, rows, kvh, row0;  // first query row of the sequence, rows of the tile from row0 on
   int32_t parts;                // CTAs of the split
-  int64_t begin, end;           // the unit's tiles among all
-  int64_t each, extra;          // tiles of a run; the first `extra` runs have one more
+  int64_t begin, end;           // the unit's places in the line
+  int64_t each, extra;          // places of a run; the first `extra` runs have one more
 };
 
 struct TreeParams {
@@ -114,8 +116,10 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s, bool fla
   return r;
 }
 
-__device__ __forceinline__ int64_t tree_weight(const TreeParams &p, const TreeSeq &q) {
-  return int64_t(q.row_tiles) * p.num_kv_heads * q.tiles;
+// What a sequence's units weigh: their tiles, and `extra` for what a unit costs
+// beside them (queries, masks, epilogue).
+__device__ __forceinline__ int64_t tree_weight(const TreeParams &p, const TreeSeq &q, int extra) {
+  return int64_t(q.row_tiles) * p.num_kv_heads * (q.tiles + extra);
 }
 
 // Block-table row of sequence s (its page j: bt[row + j * bt_s1]).
@@ -166,7 +170,7 @@ struct TreeScratch {
 
 // Sums the batch's tiles over the CTA's NT threads and finds the run of CTA
 // blockIdx.x.  Every thread returns the same run; begin == end: nothing to do.
-template <int TT, int RT, int NT>
+template <int TT, int RT, int UC, int NT>
 __device__ __forceinline__ TreeRun tree_find_run(const TreeParams &p, TreeScratch<NT> &sh) {
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -178,7 +182,7 @@ __device__ __forceinline__ TreeRun tree_find_run(const TreeParams &p, TreeScratc
   TreeSeq q = {};
   for (int s = s0; s < s1; ++s) {
     q = tree_seq<TT, RT>(p, s, blockIdx.x == 0);
-    mine += tree_weight(p, q);
+    mine += tree_weight(p, q, UC);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -211,7 +215,7 @@ __device__ __forceinline__ TreeRun tree_find_run(const TreeParams &p, TreeScratc
     if (per > 1) {
       for (; s < s1; ++s) {
         q = tree_seq<TT, RT>(p, s, false);
-        const int64_t w = tree_weight(p, q);
+        const int64_t w = tree_weight(p, q, UC);
         if (r.begin < at + w) break;
         at += w;
       }
@@ -231,11 +235,12 @@ __device__ __forceinline__ TreeRun tree_find_run(const TreeParams &p, TreeScratc
 struct TreeStretch {
   int32_t seq, kvh, row0, rows;  // rows: valid rows from row0 on, at most RT
   int32_t tile0, tile1, tiles;
+  int64_t begin;  // the unit's first place in the line
   TreeSeq q;
 };
 
 // Steps through a run stretch by stretch (one thread, or threads in step).
-template <int TT, int RT>
+template <int TT, int RT, int UC>
 struct TreeWalk {
   TreeRun run;
   int64_t pos, base;
@@ -253,36 +258,41 @@ struct TreeWalk {
   __device__ __forceinline__ bool next(const TreeParams &p, TreeStretch &s) {
     if (pos >= run.end) return false;
     int64_t w;
-    while (pos >= base + (w = tree_weight(p, q))) {
+    while (pos >= base + (w = tree_weight(p, q, UC))) {
       base += w;
       ++seq;
       q = tree_seq<TT, RT>(p, seq, false);
     }
     const int64_t off = pos - base;
-    const int64_t u = tree_div(off, q.tiles);
+    const int per = q.tiles + UC;
+    const int64_t u = tree_div(off, per);
+    const int v0 = int(off - u * per), v1 = int(min(int64_t(per), v0 + (run.end - pos)));
+    s.begin = pos - v0;
+    pos += v1 - v0;
+    if (v1 <= UC) return false;  // the run ends before the unit's tiles do begin
     s.seq = seq;
     s.q = q;
     s.kvh = q.row_tiles == 1 ? int(u) : int(tree_div(u, q.row_tiles));
     s.row0 = int(u - int64_t(s.kvh) * q.row_tiles) * RT;
     s.rows = int(min(int64_t(RT), int64_t(q.T) * p.group - s.row0));
-    s.tile0 = int(off - u * q.tiles);
-    s.tile1 = int(min(int64_t(q.tiles), s.tile0 + (run.end - pos)));
+    s.tile0 = max(0, v0 - UC);
+    s.tile1 = v1 - UC;
     s.tiles = q.tiles;
-    pos += s.tile1 - s.tile0;
     return true;
   }
 };
 
 // Describes the unit that CTA blockIdx.x's run starts inside of, for the
 // join; one thread.  `s` is the run's first stretch (null: an empty run).
+template <int UC>
 __device__ __forceinline__ void tree_write_cut(const TreeParams &p, const TreeRun &r,
                                                const TreeStretch *s) {
   TreeCut c = {};
   if (s != nullptr && s->tile0 > 0) {
-    c.begin = r.begin - s->tile0;
-    c.end = c.begin + s->tiles;
-    // the first run that starts inside the unit describes it
-    c.valid = r.start_of(int64_t(blockIdx.x) - 1) <= c.begin;
+    c.begin = s->begin;
+    c.end = c.begin + s->tiles + UC;
+    // the first run that starts between the unit's tiles describes it
+    c.valid = r.start_of(int64_t(blockIdx.x) - 1) <= c.begin + UC;
     c.q0 = s->q.q0;
     c.rows = s->rows;
     c.kvh = s->kvh;
@@ -322,6 +332,8 @@ struct TreeLogit {
 // kernel's rows (one CTA per SM).
 constexpr int kTreeSimtRows = 32, kTreeSimtTokens = 64, kTreeSimtCtasPerSm = 2;
 constexpr int kTreeTcRows = 128;
+// What a unit costs beside its tiles, in tiles.
+constexpr int kTreeSimtUnitCost = 1, kTreeTcUnitCost = 6;
 
 pkv_status_t launch_tree_simt(const TreeParams &p, int head_size, int ctas, cudaStream_t stream);
 // Queries and caches of 16 bits, and 16-bit queries over 8-bit caches.

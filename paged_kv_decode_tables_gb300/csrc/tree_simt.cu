@@ -19,7 +19,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kRT = kTreeSimtRows, kTT = kTreeSimtTokens, kThreads = 128;
+constexpr int kRT = kTreeSimtRows, kTT = kTreeSimtTokens, kUC = kTreeSimtUnitCost, kThreads = 128;
 
 template <int D>
 struct SimtCfg {
@@ -41,19 +41,19 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
   const int tid = threadIdx.x, rg = tid >> 4, tg = tid & 15;
   grid_dependency_wait();
   allow_dependent_launch();
-  const TreeRun run = tree_find_run<kTT, kRT, kThreads>(p, scratch);
+  const TreeRun run = tree_find_run<kTT, kRT, kUC, kThreads>(p, scratch);
   if (run.begin >= run.end) {
-    if (tid == 0) tree_write_cut(p, run, nullptr);
+    if (tid == 0) tree_write_cut<kUC>(p, run, nullptr);
     return;
   }
   const TreeLogit logit(p);
   const bool plain = p.cap == 0.f && p.alibi == nullptr;
-  TreeWalk<kTT, kRT> walk;
+  TreeWalk<kTT, kRT, kUC> walk;
   walk.start(p, run);
   TreeStretch st;
   bool first = true;
   while (walk.next(p, st)) {
-    if (first && tid == 0) tree_write_cut(p, run, &st);
+    if (first && tid == 0) tree_write_cut<kUC>(p, run, &st);
     // queries of the row tile (rows past the end: zeros)
     __syncthreads();
     for (int i = tid; i < kRT * D; i += kThreads) {
@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
     }
     first = false;
   }
+  if (first && tid == 0) tree_write_cut<kUC>(p, run, nullptr);
 }
 
 template <int D, int BS>

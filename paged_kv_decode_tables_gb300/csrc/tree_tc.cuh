@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
   if (warp == kScoreWarp) tc::tmem_alloc(tmem_slot, Cfg::kTmemCols);
   grid_dependency_wait();
   allow_dependent_launch();
-  const TreeRun run = tree_find_run<TT, RT, Cfg::kThreads>(p, scratch);
-  if (run.begin >= run.end && threadIdx.x == 0) tree_write_cut(p, run, nullptr);
+  const TreeRun run = tree_find_run<TT, RT, kTreeTcUnitCost, Cfg::kThreads>(p, scratch);
+  if (run.begin >= run.end && threadIdx.x == 0) tree_write_cut<kTreeTcUnitCost>(p, run, nullptr);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -909,7 +909,7 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
     const uint8_t *cache = static_cast<const uint8_t *>(kv == 0 ? p.k : p.v);
     const int64_t block_bytes = (kv == 0 ? p.k_s0 : p.v_s0) * CS;
     const int64_t head_bytes = (kv == 0 ? p.k_s1 : p.v_s1) * CS;
-    TreeWalk<TT, RT> walk;
+    TreeWalk<TT, RT, kTreeTcUnitCost> walk;
     if (kv == 0) walk.start(p, run);
     uint32_t t = 0;  // tiles issued
     int ids0 = 0, ids0_seq = -1;
@@ -923,8 +923,8 @@ __global__ void __launch_bounds__(TreeTcCfg<T, KV, D, BS>::kThreads, 1)
           d.kvh = st.kvh, d.row0 = st.row0, d.rows = st.rows;
           d.tile0 = st.tile0, d.tile1 = st.tile1, d.tiles = st.tiles;
           d.first = u == 0, d.seq = st.seq, d.shared = st.q.row_tiles > 1;
-          if (u == 0 && lane == 0) tree_write_cut(p, run, &st);
         }
+        if (u == 0 && lane == 0) tree_write_cut<kTreeTcUnitCost>(p, run, d.end ? nullptr : &st);
         if (u >= Cfg::kUnits &&
             !wait_warp(&unit_free[u % Cfg::kUnits], uint32_t(u / Cfg::kUnits - 1) & 1u)) {
           failed = true;
