@@ -332,8 +332,10 @@ struct TreeLogit {
 // kernel's rows (one CTA per SM).
 constexpr int kTreeSimtRows = 32, kTreeSimtTokens = 64, kTreeSimtCtasPerSm = 2;
 constexpr int kTreeTcRows = 128;
-// What a unit costs beside its tiles, in tiles.
-constexpr int kTreeSimtUnitCost = 1, kTreeTcUnitCost = 6;
+// What a unit costs beside its tiles, in tiles.  (Measured on 128 ragged trees of up
+// to 16 tokens / 32 of 40-64: 6 tiles 180 / 130 us, 10 tiles 188 / 122, 16 tiles 202 /
+// 126, none 230 / 185.)
+constexpr int kTreeSimtUnitCost = 1, kTreeTcUnitCost = 8;
 
 pkv_status_t launch_tree_simt(const TreeParams &p, int head_size, int ctas, cudaStream_t stream);
 // Queries and caches of 16 bits, and 16-bit queries over 8-bit caches.

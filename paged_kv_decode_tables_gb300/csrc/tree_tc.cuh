@@ -2,16 +2,16 @@
 // 16-bit or 8-bit caches (the split, the masks and the join: tree.cuh).
 //
 // One CTA per SM runs its stretches of (sequence, kv head, 128 query rows) x
-// tiles of TT tokens (128; 64 at head size 256).  Per tile
-//   S = Q K^T     M = 128 rows, N = tokens, K = head dims: both from shared memory
+// tiles of 64 tokens.  Per tile
+//   S = Q K^T     M = 128 rows, N = tokens, K = head dims: Q from tensor memory
 //   O += P V      M = 128 rows, N = head dims, K = tokens: P from tensor memory
 // with S, P and O in tensor memory.  The pages are used as they lie in the
 // cache, fetched by whole-page bulk copies:
 // - a key page [D / 8][BS][8] holds 8 tokens x 16 bytes in 128 contiguous
 //   bytes, the core matrix of an operand without swizzling: the 8-token
 //   groups number h of all pages of the tile (a page apart) make one MMA, so S
-//   comes out with its tokens permuted (column h * TT / (BS / 8) + 8 * page + i
-//   is token BS * page + 8 h + i), which a softmax does not mind;
+//   comes out with its tokens permuted at 16 tokens a page (column 32 h + 8 page
+//   + i is token 16 page + 8 h + i), which a softmax does not mind;
 // - a value page [D][BS] has rows of 16, 32 or 64 bytes of one dim's tokens:
 //   an operand with K = tokens adjacent, for 32 (64) bytes under the 32 (64)
 //   byte swizzle, which exchanges 16-byte pieces within rows; the prep warps
@@ -24,16 +24,17 @@
 // the S tile that it came from.
 //
 // Roles: warps 0-3 (and 4-7 up to head size 128) softmax, one row per thread;
-// then 4 prep warps, the copy warp, a warp for each product's MMAs.  The two softmax groups take
-// alternate tiles, each with its own running max, sum and output accumulator:
+// then 4 prep warps, a copy warp each for keys and values, a warp for each
+// product's MMAs.  The two softmax groups take alternate tiles, each with its own running max, sum and output accumulator:
 // they never wait for one another within a unit and are combined at its end.
 // The running max is lazy: it moves only when a score passes it by 2^8 (log2
 // units), and only then is the accumulator in tensor memory rescaled.
 //
-// What bounds it: at up to 128 rows a kv head the page reads from HBM (a tile
-// is 64 KiB at head size 128, about 2800 cycles of an SM's share of the HBM
-// rate; its MMAs take about 1100, its softmax about 1000 issue slots of each
-// scheduler).
+// What bounds it: at up to 128 rows a kv head and 16-bit caches the page reads
+// from HBM, 0.68-0.74 us per tile and SM at head size 128 (32 KiB; the copy
+// bandwidth's own is 0.73), of which the MMAs take 770 cycles and each of two
+// softmax groups 1500 every other tile.  8-bit caches: the widening, 1.2 us a
+// tile.  Start, end and join of a call take 25-35 us.
 //
 // Every wait is bounded, as in attention_fp8_tc.cuh: one that runs out raises a
 // CTA-wide abort flag, every role winds down, waiting (bounded) for its own
